@@ -66,6 +66,12 @@ typedef enum {
 #define VSL_MAX_SLICES 16       /* S <= 16                                  */
 #define VSL_MAX_LOGPROBS 20     /* 0 <= n_logprobs <= 20 (and <= S * V_s)   */
 #define VSL_MAX_SPEC 64         /* speculative tokens per request in vsl_verify_drafts */
+#define VSL_MAX_RANK 256        /* adapter rank in vsl_adapters_add         */
+#define VSL_MAX_VOCAB (1 << 30) /* S * V_s in the calls that score tokens and in vsl_adapters_add */
+
+/* Type of a gradient written to vocab slices. */
+#define VSL_GRAD_FP32 0
+#define VSL_GRAD_BF16 1
 
 /* Row flags written by vsl_sample (bit set = the row was not sampled).  A
  * flagged row gets token -1, logprob NaN, top-n ids -1 and top-n logprobs NaN;
@@ -310,6 +316,173 @@ VSL_API vsl_status vsl_sample_ex(const float* const* logits_slices, int32_t R, i
 VSL_API vsl_status vsl_verify_drafts(const int32_t* token_ids, const float* token_logprob,
                                      const int32_t* draft_ids, int32_t requests, int32_t spec,
                                      int32_t* out_ids, float* out_logprob, int32_t* accepted, void* stream);
+
+/* Low-rank adapters of many requests beside the shared projection.  Source:
+ * "Qwen4Exp batch-sharded sampling: inside vLLM PR #61018" (orcarouter.ai
+ * blog): upstream's flag rejects LoRA; here the rows of one batch may each use
+ * an adapter of their own. */
+
+/* Bytes of device workspace vsl_adapters_add needs (0 for non-positive sizes). */
+VSL_API size_t vsl_adapters_workspace_bytes(int32_t R, int32_t rank);
+
+/* vsl_adapters_add - adds each row's low-rank term to the base logits:
+ *   u[r][k]         = scale[a] * sum_h hidden[r][h] * A[a][k][h],  a = adapter_ids[r]
+ *   out_s[r][j]     = logits_s[r][j] + sum_k B_s[a][j][k] * u[r][k]
+ * (bf16 inputs, fp32 sums, u carried in 24 bits).  A row whose id lies outside
+ * [0, n_adapters) (-1 by convention) keeps the base logits.  A row is
+ * computed from its own hidden states, its own adapter and its own logits
+ * alone: infinities or NaNs of another row or adapter do not reach it.
+ *   logits_slices : host array of S device pointers, slice s = [R][V_s] fp32
+ *                   row-major, each 16-byte aligned (vsl_logits_local's).
+ *   out_slices    : the same layout; out_slices[s] may be logits_slices[s]
+ *                   (in place: rows without an adapter are then not touched);
+ *                   no other overlap is allowed.
+ *   hidden_bf16   : device [R][H] bf16 row-major, 16-byte aligned.
+ *   a_bf16        : device [n_adapters][rank][H] bf16, 16-byte aligned.
+ *   b_slices_bf16 : host array of S device pointers, slice s =
+ *                   [n_adapters][V_s][rank] bf16, each 16-byte aligned.
+ *   scale         : device fp32 [n_adapters] (NULL: 1).
+ *   adapter_ids   : device int32 [R].
+ *   tile_stats    : (optional, NULL) the tile statistics of out_slices, as
+ *                   vsl_tile_stats writes them, 32-byte aligned.
+ *   workspace     : device, 16-byte aligned, workspace_bytes >=
+ *                   vsl_adapters_workspace_bytes(R, rank); its contents are
+ *                   written and read by this call's kernels only.  Calls that
+ *                   can run at the same time (two streams, or two captured
+ *                   graphs) need a workspace each.
+ *   R >= 1, H >= 8 with H % 8 == 0, V_s % 4 == 0, n_adapters >= 1,
+ *   8 <= rank <= VSL_MAX_RANK with rank % 8 == 0 (adapters of lower rank are
+ *   padded with zeros), S * V_s <= VSL_MAX_VOCAB.
+ * Errors: VSL_ERR_INVALID_ARG, VSL_ERR_ALIGNMENT, VSL_ERR_UNSUPPORTED,
+ *         VSL_ERR_WORKSPACE_TOO_SMALL, VSL_ERR_CUDA. */
+VSL_API vsl_status vsl_adapters_add(const float* const* logits_slices, float* const* out_slices,
+                                    const void* hidden_bf16, int32_t R, int32_t H, int32_t S, int32_t V_s,
+                                    const void* a_bf16, const void* const* b_slices_bf16, const float* scale,
+                                    int32_t n_adapters, int32_t rank, const int32_t* adapter_ids, float* tile_stats,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Logprobs of given tokens, and the losses made of them.  With x_j = l_j / T
+ * over the whole row (all slices), p its softmax, m = max_j l_j and
+ * z = sum_j exp((l_j - m) / T):
+ *   logprob = log p_token,   entropy = -sum_j p_j log p_j.
+ * In every call below a row whose token lies outside [0, S * V_s) (-1 by
+ * convention: prompt tokens, padding, a row the sampler flagged) does not
+ * count: its outputs are 0, its gradient is 0 and its logits are not read.  A
+ * logit of -inf has probability 0.  A row with a NaN or +inf logit, or with
+ * none above -inf, gives NaN; other rows are unaffected.
+ * The temperature T is one number per call, 1e-6 <= T <= 1e6. */
+
+/* vsl_token_logprobs - the logprob (and entropy) of one given token per row.
+ *   logits_slices : as for vsl_sample (read only, one read of every logit).
+ *   token_ids : device int32 [R].
+ *   logprob   : device fp32 [R]       (output)
+ *   entropy   : device fp32 [R]       (output, may be NULL)
+ *   row_stats : device fp32 [R][2], 8-byte aligned (output, may be NULL):
+ *               (m, z), what vsl_token_logprobs_grad takes; (0, 1) for a row
+ *               that does not count.
+ * Errors: VSL_ERR_INVALID_ARG, VSL_ERR_ALIGNMENT, VSL_ERR_UNSUPPORTED,
+ *         VSL_ERR_CUDA. */
+VSL_API vsl_status vsl_token_logprobs(const float* const* logits_slices, int32_t R, int32_t S, int32_t V_s,
+                                      const int32_t* token_ids, float temperature, float* logprob, float* entropy,
+                                      float* row_stats, void* stream);
+
+/* vsl_token_logprobs_grad - the gradient of vsl_token_logprobs: for every
+ * logit, d_logprob[r] * dlogprob/dl_j + d_entropy[r] * dentropy/dl_j, with
+ *   dlogprob/dl_j = (1[j = token] - p_j) / T,
+ *   dentropy/dl_j = -p_j (log p_j + entropy) / T.
+ *   logits_slices, token_ids, temperature : those of the forward call.
+ *   row_stats   : device fp32 [R][2], from the forward call.
+ *   entropy     : device fp32 [R], from the forward call (NULL without d_entropy).
+ *   d_logprob   : device fp32 [R].
+ *   d_entropy   : device fp32 [R] (NULL: 0).
+ *   grad_slices : host array of S device pointers, slice s = [R][V_s] fp32
+ *                 (VSL_GRAD_FP32) or bf16 (VSL_GRAD_BF16) row-major, each
+ *                 16-byte aligned; fully overwritten.  fp32: grad_slices[s]
+ *                 may be logits_slices[s]; no other overlap is allowed.
+ * A row whose two derivatives are 0 gets a gradient of 0, its logits unread.
+ * Errors: VSL_ERR_INVALID_ARG, VSL_ERR_ALIGNMENT, VSL_ERR_UNSUPPORTED,
+ *         VSL_ERR_CUDA. */
+VSL_API vsl_status vsl_token_logprobs_grad(const float* const* logits_slices, int32_t R, int32_t S, int32_t V_s,
+                                           const int32_t* token_ids, float temperature, const float* row_stats,
+                                           const float* entropy, const float* d_logprob, const float* d_entropy,
+                                           void* const* grad_slices, int32_t grad_type, void* stream);
+
+/* Inputs of vsl_policy_loss (device arrays of R entries, and numbers).
+ *   token_ids    : the token each row drew.
+ *   old_logprob  : its logprob under the policy that drew it.
+ *   advantages   : A.
+ *   ref_logprob  : its logprob under the reference policy (NULL: no KL term,
+ *                  kl_coef must be 0).
+ *   weights      : w, the row's factor in the sum (1 / number of tokens, a
+ *                  loss scale, ...; NULL: 1).  A row of weight 0 does not count.
+ *   0 <= clip_low <= 1, clip_high >= 0, kl_coef and entropy_coef finite. */
+typedef struct {
+  const int32_t* token_ids;
+  const float* old_logprob;
+  const float* advantages;
+  const float* ref_logprob;
+  const float* weights;
+  float clip_low;
+  float clip_high;
+  float kl_coef;
+  float entropy_coef;
+  float temperature;
+} vsl_policy_inputs;
+
+/* Outputs of vsl_policy_loss (device arrays of R entries; all but loss may be NULL).
+ *   loss        : each row's weighted loss; the objective is their sum.
+ *   logprob, entropy : as vsl_token_logprobs.
+ *   kl          : exp(ref - logprob) - (ref - logprob) - 1 (unweighted;
+ *                 0 without ref_logprob).
+ *   grad_slices : host array of S device pointers (NULL: no gradient), as in
+ *                 vsl_token_logprobs_grad: the gradient of the sum of loss. */
+typedef struct {
+  float* loss;
+  float* logprob;
+  float* kl;
+  float* entropy;
+  void* const* grad_slices;
+  int32_t grad_type;
+} vsl_policy_outputs;
+
+/* vsl_policy_loss - clipped policy loss with a KL term and an entropy bonus,
+ * forward and backward in one call.  With ratio = exp(logprob - old_logprob)
+ * and d = ref_logprob - logprob, row r's loss is
+ *   w * ( -min(ratio * A, clip(ratio, 1 - clip_low, 1 + clip_high) * A)
+ *         + kl_coef * (exp(d) - d - 1) - entropy_coef * entropy ).
+ * Where the clipped term is the smaller one its derivative is 0; where both
+ * are equal the unclipped one's is taken.  A coefficient of 0 leaves its term
+ * out (an infinite KL then does not matter).
+ * Errors: VSL_ERR_INVALID_ARG, VSL_ERR_ALIGNMENT, VSL_ERR_UNSUPPORTED,
+ *         VSL_ERR_CUDA. */
+VSL_API vsl_status vsl_policy_loss(const float* const* logits_slices, int32_t R, int32_t S, int32_t V_s,
+                                   const vsl_policy_inputs* inputs, const vsl_policy_outputs* outputs, void* stream);
+
+/* vsl_preference_loss - preference loss of pairs of sequences over the
+ * logprobs of their tokens, and its gradient.  Sequence i owns rows
+ * [offsets[i], offsets[i + 1]) and pair q prefers sequence 2q to 2q + 1.  With
+ * s_i = beta * sum over its rows of (logprob - ref_logprob), h = s_2q - s_2q+1
+ * and e = label_smoothing,
+ *   loss[q] = w * ( -(1 - e) log sigmoid(h) - e log sigmoid(-h) ).
+ *   logprob     : device fp32 [R] (vsl_token_logprobs: 0 where a row does not count)
+ *   ref_logprob : device fp32 [R] (NULL: 0)
+ *   offsets     : device int32 [2 * pairs + 1], non-decreasing, 0 <= offsets <= R
+ *                 (values outside are read as the nearest of the two; an
+ *                 empty sequence sums to 0)
+ *   weights     : device fp32 [pairs] (NULL: 1).  A pair of weight 0 does not
+ *                 count: loss, rewards and derivatives 0, its rows unread.
+ *   loss        : device fp32 [pairs]     (output)
+ *   rewards     : device fp32 [pairs][2]  (output, may be NULL) s_2q, s_2q+1
+ *   d_logprob   : device fp32 [R]         (output, may be NULL) the derivative
+ *                 of the sum of loss by logprob: for vsl_token_logprobs_grad;
+ *                 0 in rows before the first sequence and behind the last
+ *   R >= 0, pairs >= 1, beta finite, 0 <= label_smoothing <= 1.
+ * Errors: VSL_ERR_INVALID_ARG, VSL_ERR_UNSUPPORTED (pairs above 2^30 - 1),
+ *         VSL_ERR_CUDA. */
+VSL_API vsl_status vsl_preference_loss(const float* logprob, const float* ref_logprob, const int32_t* offsets,
+                                       const float* weights, int32_t R, int32_t pairs, float beta,
+                                       float label_smoothing, float* loss, float* rewards, float* d_logprob,
+                                       void* stream);
 
 /* Reads and clears the device error word the kernels set when a bounded wait
  * gives up (a bug, never expected).  Synchronises the current device.

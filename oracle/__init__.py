@@ -34,6 +34,10 @@ reordering beyond what the definition states:
   statistics the projection can emit tile by tile so that the sampler reads
   only the tiles that can hold its candidates (a reading of the same section;
   the record is the library's, stated in the module).
+* ``oracle.adapters`` - the low-rank adapters beside the projection, row by row
+  (the pages' flag rejects LoRA; the formula is the adapters' definition).
+* ``oracle.scores``   - the logprobs and entropies of given tokens, their
+  gradient, the clipped policy loss with its KL term and the preference loss.
 * ``oracle.timing``   - the harness that times the sampler oracle on the
   host's cores for the CPU baseline (no arithmetic of the method).
 
@@ -44,6 +48,8 @@ probabilities == 1), exact integer GEMMs, and chi-square tests of the draw
 frequencies; the processed logprobs against the library log-softmax (full
 vocabulary), point masses, and the frequencies of the oracle's own draws; the
 verification against an independent formulation and, by sampling, against
-the rejection rule it implements for a point-mass draft.
+the rejection rule it implements for a point-mass draft; the adapters against
+the merged weights W + scale B A; the logprobs against scipy, the gradients
+against central differences, the losses against their closed forms.
 No function here is "parity unpinned".
 """

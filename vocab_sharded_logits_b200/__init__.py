@@ -13,7 +13,9 @@ import torch
 __all__ = [
     "logits_local", "tile_stats", "tile_stats_shape", "sample", "sample_launches", "sample_plan", "make_row_params", "SampleResult", "lib", "status_string",
     "device_error", "VslError", "verify_drafts", "VerifyResult", "MAX_SPEC", "ROW_NONFINITE", "ROW_ALL_NEG_INF", "ROW_BAD_TEMPERATURE",
-    "ROW_BAD_TOP_P", "ROW_BAD_TOP_K", "ROW_SCALE_OVERFLOW", "MAX_SLICES", "MAX_LOGPROBS",
+    "ROW_BAD_TOP_P", "ROW_BAD_TOP_K", "ROW_SCALE_OVERFLOW", "MAX_SLICES", "MAX_LOGPROBS", "MAX_RANK", "adapters_add",
+    "adapters_workspace_bytes", "token_logprobs", "token_logprobs_grad", "TokenLogprobs", "policy_loss", "PolicyLoss",
+    "preference_loss", "PreferenceLoss",
 ]
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "libvsl.so")
 MAX_SLICES = 16
 MAX_LOGPROBS = 20
 MAX_SPEC = 64
+MAX_RANK = 256
 ROW_NONFINITE = 1 << 0
 ROW_ALL_NEG_INF = 1 << 1
 ROW_BAD_TEMPERATURE = 1 << 2
@@ -45,6 +48,18 @@ class _Extras(ctypes.Structure):
     _fields_ = [("kept_theta", ctypes.c_void_p), ("processed_logprob", ctypes.c_void_p),
                 ("processed_topn_ids", ctypes.c_void_p), ("processed_topn_logprob", ctypes.c_void_p),
                 ("tile_stats", ctypes.c_void_p)]
+
+
+class _PolicyInputs(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("token_ids", "old_logprob", "advantages", "ref_logprob",
+                                                     "weights")] + \
+               [(name, ctypes.c_float) for name in ("clip_low", "clip_high", "kl_coef", "entropy_coef", "temperature")]
+
+
+class _PolicyOutputs(ctypes.Structure):
+    _fields_ = [("loss", ctypes.c_void_p), ("logprob", ctypes.c_void_p), ("kl", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("grad_slices", ctypes.POINTER(ctypes.c_void_p)),
+                ("grad_type", ctypes.c_int32)]
 
 
 class _Plan(ctypes.Structure):
@@ -79,6 +94,22 @@ def _load():
                                 ctypes.POINTER(_Extras), vp]
     l.vsl_verify_drafts.restype = ctypes.c_int
     l.vsl_verify_drafts.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, vp]
+    f32 = ctypes.c_float
+    l.vsl_adapters_workspace_bytes.restype = sz
+    l.vsl_adapters_workspace_bytes.argtypes = [i32, i32]
+    l.vsl_adapters_add.restype = ctypes.c_int
+    l.vsl_adapters_add.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), vp, i32, i32, i32, i32, vp,
+                                   ctypes.POINTER(vp), vp, i32, i32, vp, vp, vp, sz, vp]
+    l.vsl_token_logprobs.restype = ctypes.c_int
+    l.vsl_token_logprobs.argtypes = [ctypes.POINTER(vp), i32, i32, i32, vp, f32, vp, vp, vp, vp]
+    l.vsl_token_logprobs_grad.restype = ctypes.c_int
+    l.vsl_token_logprobs_grad.argtypes = [ctypes.POINTER(vp), i32, i32, i32, vp, f32, vp, vp, vp, vp,
+                                          ctypes.POINTER(vp), i32, vp]
+    l.vsl_policy_loss.restype = ctypes.c_int
+    l.vsl_policy_loss.argtypes = [ctypes.POINTER(vp), i32, i32, i32, ctypes.POINTER(_PolicyInputs),
+                                  ctypes.POINTER(_PolicyOutputs), vp]
+    l.vsl_preference_loss.restype = ctypes.c_int
+    l.vsl_preference_loss.argtypes = [vp, vp, vp, vp, i32, i32, f32, f32, vp, vp, vp, vp]
     l.vsl_device_error.restype = ctypes.c_int
     l.vsl_device_error.argtypes = [ctypes.POINTER(u32)]
     l.vsl_status_string.restype = ctypes.c_char_p
@@ -332,6 +363,244 @@ def verify_drafts(token_ids, draft_ids, token_logprob=None, out=None, stream=Non
                                        _ptr(out.out_logprob) if token_logprob is not None else None,
                                        _ptr(out.accepted), _stream_handle(stream, dev))
     _check(status, "vsl_verify_drafts")
+    return out
+
+
+def _slices(logits_slices, where):
+    """(R, S, V_s, device) of fp32 logits slices."""
+    R, V_s = logits_slices[0].shape
+    dev = logits_slices[0].device
+    for t in logits_slices:
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != (R, V_s) or t.device != dev:
+            raise ValueError(f"{where}: logits slices must be contiguous fp32 [R, V_s] on one device")
+    return R, len(logits_slices), V_s, dev
+
+
+def _rows(t, name, dtype, shape, dev):
+    """Checks a per-row tensor (None passes)."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev):
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {dev}")
+    return t
+
+
+def _grad_slices(grad, grad_dtype, R, S, V_s, dev):
+    """The gradient's slices (allocated when not given) and their VSL_GRAD_* type."""
+    if grad is None:
+        grad = list(torch.empty(S, R, V_s, dtype=grad_dtype, device=dev).unbind(0)) if R * V_s % 8 == 0 else \
+            [torch.empty(R, V_s, dtype=grad_dtype, device=dev) for _ in range(S)]
+    if len(grad) != S:
+        raise ValueError(f"grad must hold {S} slices")
+    dtype = grad[0].dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("the gradient is float32 or bfloat16")
+    for t in grad:
+        _rows(t, "grad slices", dtype, (R, V_s), dev)
+    return grad, 1 if dtype == torch.bfloat16 else 0
+
+
+def adapters_workspace_bytes(R, rank):
+    """Bytes of device workspace one ``adapters_add`` call needs."""
+    return lib.vsl_adapters_workspace_bytes(int(R), int(rank))
+
+
+def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, out=None, stream=None, tile_stats=None,
+                 workspace=None):
+    """Adds each row's low-rank adapter to the base logits of ``logits_local``:
+    ``out[s][r] = logits[s][r] + b[s][i] @ (scale[i] * (a[i] @ hidden[r]))``, i = ``adapter_ids[r]``.
+
+    hidden: bf16 [R, H]; a: bf16 [n, rank, H]; b_slices: list of bf16 [n, V_s, rank]; adapter_ids:
+    int32 [R] (outside [0, n), -1 by convention: the row keeps its base logits); scale: fp32 [n]
+    (None: 1).  rank is a multiple of 8 up to MAX_RANK.  ``out`` may be ``logits_slices`` (in place).
+    With ``tile_stats`` (True, or a tensor to fill) the tile statistics of the result are written
+    too, and the call returns ``(slices, stats)``.  workspace: a uint8 tensor of
+    ``adapters_workspace_bytes(R, rank)`` bytes (None: allocated for the call); calls that may run
+    at the same time need one each.
+    """
+    R, S, V_s, dev = _slices(logits_slices, "adapters_add")
+    n, rank, H = a.shape
+    if hidden.dtype != torch.bfloat16 or a.dtype != torch.bfloat16 or any(b.dtype != torch.bfloat16 for b in b_slices):
+        raise TypeError("hidden states and adapters must be bfloat16")
+    _rows(hidden, "hidden", torch.bfloat16, (R, H), dev)
+    _rows(a, "a", torch.bfloat16, (n, rank, H), dev)
+    if len(b_slices) != S:
+        raise ValueError(f"b_slices must hold {S} slices")
+    for b in b_slices:
+        _rows(b, "b_slices", torch.bfloat16, (n, V_s, rank), dev)
+    _rows(adapter_ids, "adapter_ids", torch.int32, (R,), dev)
+    _rows(scale, "scale", torch.float32, (n,), dev)
+    if out is None:
+        out = [torch.empty_like(t) for t in logits_slices]
+    if len(out) != S:
+        raise ValueError(f"out must hold {S} slices")
+    for t in out:
+        _rows(t, "out", torch.float32, (R, V_s), dev)
+    stats = None if tile_stats is None or tile_stats is False else _stats_tensor(tile_stats, R, S, V_s, dev)
+    with _on_device(dev):
+        if workspace is None:
+            # from the pool of the stream that uses it
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(adapters_workspace_bytes(R, rank), dtype=torch.uint8, device=dev)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+        status = lib.vsl_adapters_add(_ptr_array(logits_slices), _ptr_array(out), _ptr(hidden), R, H, S, V_s, _ptr(a),
+                                      _ptr_array(b_slices), _ptr(scale), n, rank, _ptr(adapter_ids), _ptr(stats),
+                                      _ptr(workspace), workspace.numel(), _stream_handle(stream, dev))
+    _check(status, "vsl_adapters_add")
+    return out if stats is None else (out, stats)
+
+
+class TokenLogprobs:
+    """Outputs of ``token_logprobs``: logprob [R], entropy [R] (when asked for), row_stats [R, 2]
+    (the row's largest logit m and sum of exp((l - m) / T)) and the temperature they hold for."""
+
+    def __init__(self, logprob, entropy, row_stats, temperature):
+        self.logprob = logprob
+        self.entropy = entropy
+        self.row_stats = row_stats
+        self.temperature = temperature
+
+
+def token_logprobs(logits_slices, token_ids, temperature=1.0, entropy=False, out=None, stream=None):
+    """Logprob of one given token per row, over the whole vocabulary at ``temperature``; optionally
+    the row's entropy.
+
+    logits_slices: list of fp32 [R, V_s] CUDA tensors; token_ids: int32 [R] (outside the vocabulary,
+    -1 by convention: the row does not count, its outputs are 0).
+    """
+    R, S, V_s, dev = _slices(logits_slices, "token_logprobs")
+    _rows(token_ids, "token_ids", torch.int32, (R,), dev)
+    if out is None:
+        out = TokenLogprobs(torch.empty(R, device=dev), torch.empty(R, device=dev) if entropy else None,
+                            torch.empty(R, 2, device=dev), float(temperature))
+    out.temperature = float(temperature)
+    _rows(out.logprob, "out.logprob", torch.float32, (R,), dev)
+    _rows(out.entropy, "out.entropy", torch.float32, (R,), dev)
+    _rows(out.row_stats, "out.row_stats", torch.float32, (R, 2), dev)
+    if entropy and out.entropy is None:
+        raise ValueError("out.entropy is missing")
+    with _on_device(dev):
+        status = lib.vsl_token_logprobs(_ptr_array(logits_slices), R, S, V_s, _ptr(token_ids), out.temperature,
+                                        _ptr(out.logprob), _ptr(out.entropy) if entropy else None,
+                                        _ptr(out.row_stats), _stream_handle(stream, dev))
+    _check(status, "vsl_token_logprobs")
+    return out
+
+
+def token_logprobs_grad(logits_slices, token_ids, forward, d_logprob, d_entropy=None, grad=None,
+                        grad_dtype=torch.float32, stream=None):
+    """Gradient of ``token_logprobs``: per logit, ``d_logprob * dlogprob/dl + d_entropy * dentropy/dl``.
+
+    logits_slices, token_ids: the forward call's; forward: its ``TokenLogprobs`` (with the entropy
+    when d_entropy is given); d_logprob, d_entropy: fp32 [R].  Returns the S slices [R, V_s] in
+    ``grad_dtype`` (``grad`` if given; fp32 slices may be the logits themselves).
+    """
+    R, S, V_s, dev = _slices(logits_slices, "token_logprobs_grad")
+    _rows(token_ids, "token_ids", torch.int32, (R,), dev)
+    _rows(forward.row_stats, "forward.row_stats", torch.float32, (R, 2), dev)
+    _rows(d_logprob, "d_logprob", torch.float32, (R,), dev)
+    _rows(d_entropy, "d_entropy", torch.float32, (R,), dev)
+    if d_entropy is not None and forward.entropy is None:
+        raise ValueError("d_entropy needs a forward call with entropy=True")
+    grad, kind = _grad_slices(grad, grad_dtype, R, S, V_s, dev)
+    ent = _rows(forward.entropy, "forward.entropy", torch.float32, (R,), dev) if d_entropy is not None else None
+    with _on_device(dev):
+        status = lib.vsl_token_logprobs_grad(_ptr_array(logits_slices), R, S, V_s, _ptr(token_ids),
+                                             forward.temperature, _ptr(forward.row_stats), _ptr(ent),
+                                             _ptr(d_logprob), _ptr(d_entropy), _ptr_array(grad), kind,
+                                             _stream_handle(stream, dev))
+    _check(status, "vsl_token_logprobs_grad")
+    return grad
+
+
+class PolicyLoss:
+    """Outputs of ``policy_loss``: per row its weighted loss, logprob, KL estimate and entropy, and
+    the gradient slices of the sum of the losses (None when not asked for)."""
+
+    def __init__(self, loss, logprob, kl, entropy, grad):
+        self.loss = loss
+        self.logprob = logprob
+        self.kl = kl
+        self.entropy = entropy
+        self.grad = grad
+
+
+def policy_loss(logits_slices, token_ids, old_logprob, advantages, weights=None, ref_logprob=None, clip_low=0.2,
+                clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, temperature=1.0, grad=True, grad_dtype=torch.float32,
+                stream=None):
+    """Clipped policy loss with a KL term and an entropy bonus, and its gradient by the logits.
+
+    With ratio = exp(logprob - old_logprob) and d = ref_logprob - logprob, each row's loss is
+    ``w * (-min(ratio * A, clip(ratio, 1 - clip_low, 1 + clip_high) * A) + kl_coef * (exp(d) - d - 1)
+    - entropy_coef * entropy)``; the objective is the rows' sum.  All row inputs are fp32 [R]
+    (token_ids int32 [R]); rows with weight 0 or a token outside the vocabulary do not count.
+    grad: True (allocated in ``grad_dtype``), False / None (forward only) or S slices to fill (fp32
+    slices may be the logits themselves).
+    """
+    R, S, V_s, dev = _slices(logits_slices, "policy_loss")
+    _rows(token_ids, "token_ids", torch.int32, (R,), dev)
+    for t, name in ((old_logprob, "old_logprob"), (advantages, "advantages"), (weights, "weights"),
+                    (ref_logprob, "ref_logprob")):
+        _rows(t, name, torch.float32, (R,), dev)
+    kind = 0
+    if grad is True:
+        grad = None
+    elif grad is None or grad is False:
+        grad = False
+    if grad is not False:
+        grad, kind = _grad_slices(grad, grad_dtype, R, S, V_s, dev)
+    rows = torch.empty(4, R, device=dev).unbind(0)
+    out = PolicyLoss(*rows, grad if grad is not False else None)
+    i = _PolicyInputs(_addr(token_ids), _addr(old_logprob), _addr(advantages), _addr(ref_logprob), _addr(weights),
+                      clip_low, clip_high, kl_coef, entropy_coef, temperature)
+    o = _PolicyOutputs(*[t.data_ptr() for t in rows])
+    o.grad_type = kind
+    if out.grad is not None:
+        o.grad_slices = _ptr_array(out.grad)
+    with _on_device(dev):
+        status = lib.vsl_policy_loss(_ptr_array(logits_slices), R, S, V_s, ctypes.byref(i), ctypes.byref(o),
+                                     _stream_handle(stream, dev))
+    _check(status, "vsl_policy_loss")
+    return out
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+class PreferenceLoss:
+    """Outputs of ``preference_loss``: per pair its weighted loss and the two sequences' rewards
+    [pairs, 2]; per row the derivative of the losses' sum by the logprob."""
+
+    def __init__(self, loss, rewards, d_logprob):
+        self.loss = loss
+        self.rewards = rewards
+        self.d_logprob = d_logprob
+
+
+def preference_loss(logprob, ref_logprob, offsets, beta, label_smoothing=0.0, weights=None, stream=None):
+    """Preference loss of pairs of sequences (paired log ratios) over ``token_logprobs``' logprobs.
+
+    Sequence i owns rows [offsets[i], offsets[i + 1]); pair q prefers sequence 2q to 2q + 1; with
+    s_i = beta * sum(logprob - ref_logprob) and h = s_2q - s_2q+1 its loss is
+    ``w * (-(1 - e) log sigmoid(h) - e log sigmoid(-h))``, e = label_smoothing.
+    logprob, ref_logprob (None: 0): fp32 [R]; offsets: int32 [2 * pairs + 1], non-decreasing, on the
+    device; weights: fp32 [pairs].  ``d_logprob`` goes to ``token_logprobs_grad``.
+    """
+    dev = logprob.device
+    R = logprob.numel()
+    pairs = (offsets.numel() - 1) // 2
+    _rows(logprob, "logprob", torch.float32, (R,), dev)
+    _rows(ref_logprob, "ref_logprob", torch.float32, (R,), dev)
+    if offsets.numel() < 3 or offsets.numel() % 2 == 0:
+        raise ValueError("offsets must hold 2 * pairs + 1 entries")
+    _rows(offsets, "offsets", torch.int32, (2 * pairs + 1,), dev)
+    _rows(weights, "weights", torch.float32, (pairs,), dev)
+    out = PreferenceLoss(torch.empty(pairs, device=dev), torch.empty(pairs, 2, device=dev), torch.empty(R, device=dev))
+    with _on_device(dev):
+        status = lib.vsl_preference_loss(_ptr(logprob), _ptr(ref_logprob), _ptr(offsets), _ptr(weights), R, pairs,
+                                         beta, label_smoothing, _ptr(out.loss), _ptr(out.rewards),
+                                         _ptr(out.d_logprob), _stream_handle(stream, dev))
+    _check(status, "vsl_preference_loss")
     return out
 
 

@@ -1,7 +1,8 @@
 // vsl_api.cu - the extern "C" entry points of libvsl: host-side argument
-// validation, then a launch of the projection or the sampler kernel.
+// validation, then a launch of the call's kernels.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "vsl_internal.h"
@@ -20,6 +21,35 @@ uint32_t* device_error_word() {
 namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// The checks every call that reads logits slices and scores tokens makes.
+vsl_status check_slices(const float* const* logits, int32_t R, int32_t S, int32_t V_s) {
+  if (logits == nullptr || R <= 0 || S <= 0 || V_s <= 0) return VSL_ERR_INVALID_ARG;
+  if (S > VSL_MAX_SLICES || static_cast<long long>(S) * V_s > VSL_MAX_VOCAB) return VSL_ERR_UNSUPPORTED;
+  if (V_s % 4 != 0) return VSL_ERR_ALIGNMENT;
+  for (int s = 0; s < S; ++s) {
+    if (logits[s] == nullptr) return VSL_ERR_INVALID_ARG;
+    if (!aligned16(logits[s])) return VSL_ERR_ALIGNMENT;
+  }
+  return VSL_OK;
+}
+
+// Output slices: aligned, distinct, and no alias of the logits but (where
+// allowed) the slice of the same index.
+vsl_status check_out_slices(const float* const* logits, void* const* out, int32_t S, bool in_place_allowed) {
+  for (int s = 0; s < S; ++s) {
+    if (out[s] == nullptr) return VSL_ERR_INVALID_ARG;
+    if (!aligned16(out[s])) return VSL_ERR_ALIGNMENT;
+    for (int o = 0; o < S; ++o) {
+      if (out[s] == static_cast<const void*>(logits[o]) && !(in_place_allowed && o == s)) return VSL_ERR_INVALID_ARG;
+      if (o < s && out[o] == out[s]) return VSL_ERR_INVALID_ARG;
+    }
+  }
+  return VSL_OK;
+}
+
+bool temperature_ok(float t) { return t >= 1e-6f && t <= 1e6f; }
 }  // namespace
 
 }  // namespace vsl
@@ -165,6 +195,110 @@ vsl_status vsl_verify_drafts(const int32_t* token_ids, const float* token_logpro
   if (static_cast<long long>(requests) * (spec + 1) > 0x7FFFFFFFLL) return VSL_ERR_UNSUPPORTED;
   const cudaError_t e = vsl::launch_verify(token_ids, token_logprob, draft_ids, requests, spec, out_ids,
                                            out_logprob, accepted, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSL_OK : VSL_ERR_CUDA;
+}
+
+size_t vsl_adapters_workspace_bytes(int32_t R, int32_t rank) {
+  if (R <= 0 || rank <= 0) return 0;
+  return vsl::adapters_workspace_bytes(R, rank);
+}
+
+vsl_status vsl_adapters_add(const float* const* logits_slices, float* const* out_slices, const void* hidden_bf16,
+                            int32_t R, int32_t H, int32_t S, int32_t V_s, const void* a_bf16,
+                            const void* const* b_slices_bf16, const float* scale, int32_t n_adapters, int32_t rank,
+                            const int32_t* adapter_ids, float* tile_stats, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (out_slices == nullptr || hidden_bf16 == nullptr || a_bf16 == nullptr || b_slices_bf16 == nullptr ||
+      adapter_ids == nullptr)
+    return VSL_ERR_INVALID_ARG;
+  if (H <= 0 || n_adapters <= 0 || rank <= 0) return VSL_ERR_INVALID_ARG;
+  vsl_status st = vsl::check_slices(logits_slices, R, S, V_s);
+  if (st != VSL_OK) return st;
+  if (rank > VSL_MAX_RANK) return VSL_ERR_UNSUPPORTED;
+  if (H % 8 != 0 || rank % 8 != 0) return VSL_ERR_ALIGNMENT;
+  if (!vsl::aligned16(hidden_bf16) || !vsl::aligned16(a_bf16)) return VSL_ERR_ALIGNMENT;
+  for (int s = 0; s < S; ++s) {
+    if (b_slices_bf16[s] == nullptr) return VSL_ERR_INVALID_ARG;
+    if (!vsl::aligned16(b_slices_bf16[s])) return VSL_ERR_ALIGNMENT;
+  }
+  void* out[VSL_MAX_SLICES];
+  for (int s = 0; s < S; ++s) out[s] = out_slices[s];
+  st = vsl::check_out_slices(logits_slices, out, S, true);
+  if (st != VSL_OK) return st;
+  if (tile_stats != nullptr && !vsl::aligned32(tile_stats)) return VSL_ERR_ALIGNMENT;
+  if (workspace == nullptr) return VSL_ERR_INVALID_ARG;
+  if (!vsl::aligned16(workspace)) return VSL_ERR_ALIGNMENT;
+  if (workspace_bytes < vsl_adapters_workspace_bytes(R, rank)) return VSL_ERR_WORKSPACE_TOO_SMALL;
+  const cudaError_t e =
+      vsl::launch_adapters_add(logits_slices, out_slices, hidden_bf16, R, H, S, V_s, a_bf16, b_slices_bf16, scale,
+                               n_adapters, rank, adapter_ids, tile_stats, workspace, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSL_OK : VSL_ERR_CUDA;
+}
+
+vsl_status vsl_token_logprobs(const float* const* logits_slices, int32_t R, int32_t S, int32_t V_s,
+                              const int32_t* token_ids, float temperature, float* logprob, float* entropy,
+                              float* row_stats, void* stream) {
+  if (token_ids == nullptr || logprob == nullptr || !vsl::temperature_ok(temperature)) return VSL_ERR_INVALID_ARG;
+  const vsl_status st = vsl::check_slices(logits_slices, R, S, V_s);
+  if (st != VSL_OK) return st;
+  if (row_stats != nullptr && !vsl::aligned8(row_stats)) return VSL_ERR_ALIGNMENT;
+  const cudaError_t e = vsl::launch_token_logprobs(logits_slices, R, S, V_s, token_ids, temperature, logprob, entropy,
+                                                   row_stats, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSL_OK : VSL_ERR_CUDA;
+}
+
+vsl_status vsl_token_logprobs_grad(const float* const* logits_slices, int32_t R, int32_t S, int32_t V_s,
+                                   const int32_t* token_ids, float temperature, const float* row_stats,
+                                   const float* entropy, const float* d_logprob, const float* d_entropy,
+                                   void* const* grad_slices, int32_t grad_type, void* stream) {
+  if (token_ids == nullptr || row_stats == nullptr || d_logprob == nullptr || grad_slices == nullptr)
+    return VSL_ERR_INVALID_ARG;
+  if (d_entropy != nullptr && entropy == nullptr) return VSL_ERR_INVALID_ARG;
+  if (!vsl::temperature_ok(temperature)) return VSL_ERR_INVALID_ARG;
+  if (grad_type != VSL_GRAD_FP32 && grad_type != VSL_GRAD_BF16) return VSL_ERR_INVALID_ARG;
+  vsl_status st = vsl::check_slices(logits_slices, R, S, V_s);
+  if (st != VSL_OK) return st;
+  st = vsl::check_out_slices(logits_slices, grad_slices, S, grad_type == VSL_GRAD_FP32);
+  if (st != VSL_OK) return st;
+  if (!vsl::aligned8(row_stats)) return VSL_ERR_ALIGNMENT;
+  const cudaError_t e =
+      vsl::launch_token_logprobs_grad(logits_slices, R, S, V_s, token_ids, temperature, row_stats, entropy, d_logprob,
+                                      d_entropy, grad_slices, grad_type, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSL_OK : VSL_ERR_CUDA;
+}
+
+vsl_status vsl_policy_loss(const float* const* logits_slices, int32_t R, int32_t S, int32_t V_s,
+                           const vsl_policy_inputs* inputs, const vsl_policy_outputs* outputs, void* stream) {
+  if (inputs == nullptr || outputs == nullptr) return VSL_ERR_INVALID_ARG;
+  if (inputs->token_ids == nullptr || inputs->old_logprob == nullptr || inputs->advantages == nullptr ||
+      outputs->loss == nullptr)
+    return VSL_ERR_INVALID_ARG;
+  if (!vsl::temperature_ok(inputs->temperature)) return VSL_ERR_INVALID_ARG;
+  // written so that a NaN is refused
+  if (!(inputs->clip_low >= 0.0f && inputs->clip_low <= 1.0f) || !(inputs->clip_high >= 0.0f)) return VSL_ERR_INVALID_ARG;
+  if (!std::isfinite(inputs->kl_coef) || !std::isfinite(inputs->entropy_coef)) return VSL_ERR_INVALID_ARG;
+  if (inputs->kl_coef != 0.0f && inputs->ref_logprob == nullptr) return VSL_ERR_INVALID_ARG;
+  if (outputs->grad_type != VSL_GRAD_FP32 && outputs->grad_type != VSL_GRAD_BF16) return VSL_ERR_INVALID_ARG;
+  vsl_status st = vsl::check_slices(logits_slices, R, S, V_s);
+  if (st != VSL_OK) return st;
+  if (outputs->grad_slices != nullptr) {
+    st = vsl::check_out_slices(logits_slices, outputs->grad_slices, S, outputs->grad_type == VSL_GRAD_FP32);
+    if (st != VSL_OK) return st;
+  }
+  const cudaError_t e =
+      vsl::launch_policy_loss(logits_slices, R, S, V_s, *inputs, *outputs, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VSL_OK : VSL_ERR_CUDA;
+}
+
+vsl_status vsl_preference_loss(const float* logprob, const float* ref_logprob, const int32_t* offsets,
+                               const float* weights, int32_t R, int32_t pairs, float beta, float label_smoothing,
+                               float* loss, float* rewards, float* d_logprob, void* stream) {
+  if (offsets == nullptr || loss == nullptr || R < 0 || pairs <= 0) return VSL_ERR_INVALID_ARG;
+  if (R > 0 && logprob == nullptr) return VSL_ERR_INVALID_ARG;
+  if (!std::isfinite(beta) || !(label_smoothing >= 0.0f && label_smoothing <= 1.0f)) return VSL_ERR_INVALID_ARG;
+  if (pairs > 0x3FFFFFFF) return VSL_ERR_UNSUPPORTED;  // 2 * pairs + 1 offsets
+  const cudaError_t e = vsl::launch_preference(logprob, ref_logprob, offsets, weights, R, pairs, beta, label_smoothing,
+                                               loss, rewards, d_logprob, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VSL_OK : VSL_ERR_CUDA;
 }
 

@@ -40,6 +40,27 @@ cudaError_t launch_verify(const int32_t* token_ids, const float* token_logprob, 
                           int requests, int spec, int32_t* out_ids, float* out_logprob, int32_t* accepted,
                           cudaStream_t stream);
 
+// Low-rank adapters: workspace and launch.  Arguments already validated.
+size_t adapters_workspace_bytes(int R, int rank);
+cudaError_t launch_adapters_add(const float* const* logits, float* const* out, const void* hidden, int R, int H, int S,
+                                int V_s, const void* a, const void* const* b, const float* scale, int n, int rank,
+                                const int32_t* ids, float* stats, void* workspace, cudaStream_t stream);
+
+// Logprobs of given tokens, their gradient, and the losses made of them.
+// Arguments already validated.
+cudaError_t launch_token_logprobs(const float* const* logits, int R, int S, int V_s, const int32_t* token_ids,
+                                  float temperature, float* logprob, float* entropy, float* row_stats,
+                                  cudaStream_t stream);
+cudaError_t launch_token_logprobs_grad(const float* const* logits, int R, int S, int V_s, const int32_t* token_ids,
+                                       float temperature, const float* row_stats, const float* entropy,
+                                       const float* d_logprob, const float* d_entropy, void* const* grad,
+                                       int grad_type, cudaStream_t stream);
+cudaError_t launch_policy_loss(const float* const* logits, int R, int S, int V_s, const vsl_policy_inputs& in,
+                               const vsl_policy_outputs& out, cudaStream_t stream);
+cudaError_t launch_preference(const float* logprob, const float* ref, const int32_t* offsets, const float* weights,
+                              int R, int pairs, float beta, float smoothing, float* loss, float* rewards,
+                              float* d_logprob, cudaStream_t stream);
+
 // Sampler launch geometry for a vocabulary of V tokens on a device that
 // schedules clusters of at most maxc CTAs: CTAs per row (cluster size) and
 // elements per CTA.  Returns false if V cannot be handled.
