@@ -9,14 +9,15 @@
 //   d H / d l_j       = -p_j (log p_j + H) / T,
 // so the gradient of any function of a row's logprob and entropy is
 //   G_j = (g 1[j = t] - p_j (g + h (log p_j + H))) / T,  g = df / dlogp, h = df / dH,
-// and with p_j = e_j / z, log p_j = (l_j - m) / T - log z:
-//   G_j = e_j (alpha + gamma (l_j - m)) + (g / T) 1[j = t].
+// and with p_j = e_j / z, log p_j = log e_j - log z:
+//   G_j = e_j (alpha + gamma log e_j) + (g / T) 1[j = t].
 // Clipped policy loss of a row with ratio r = exp(logp - old):
 //   w [ -min(r A, clip(r, 1 - lo, 1 + hi) A) + beta (exp(d) - d - 1) - c H ],  d = ref - logp.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "vsl_internal.h"
 #include "vsl_ptx.cuh"
@@ -26,9 +27,10 @@ namespace vsl {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;  // units of four logits a thread has in flight
+constexpr int kThreads = 512;  // forward and gradient kernels
+constexpr int kPolicyCtas = 3; // CTAs of the policy kernel that stand on an SM
+constexpr int kBatch = 4;      // units of four logits a thread has in flight
+constexpr int kMaxCluster = 8;
 
 struct SliceArgs {
   const float* slices[VSL_MAX_SLICES];
@@ -36,62 +38,107 @@ struct SliceArgs {
   int units;      // S * V_s / 4
   int V_s;
   ExpScale c;
-  float temperature;
 };
 
 __device__ __forceinline__ const float* unit_ptr(const SliceArgs& a, int row, const SliceCursor& k) {
   return a.slices[k.slice] + static_cast<size_t>(row) * a.V_s + 4 * static_cast<size_t>(k.at);
 }
 
-// 16-byte load of data read once (not the read-only path: the gradient may be
-// written over the logits by the same kernel).
-__device__ __forceinline__ float4 ldg_once4(const float* p) {
-  float4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// Statistics of units [first, last) of a row by the whole CTA.
-template <bool ENT>
-__device__ __forceinline__ SoftmaxStats part_stats(const SliceArgs& a, int row, int first, int last) {
-  SoftmaxStats s = stats_empty();
-  int i = first + static_cast<int>(threadIdx.x);
+// Position and loads of a thread over units [first, last) of a row.
+struct UnitReader {
   SliceCursor k;
-  k.start(i < last ? i : first, a.per_slice);
-  const int step = static_cast<int>(blockDim.x);
-  while (i < last) {
-    float v[4 * kBatch];
+  int i, last, step;
+  __device__ __forceinline__ UnitReader(const SliceArgs& a, int first, int last_, int thread, int threads)
+      : i(first + thread), last(last_), step(threads) {
+    k.start(i < last ? i : 0, a.per_slice);
+  }
+  // The next kBatch units (-inf past the end).
+  __device__ __forceinline__ void load(const SliceArgs& a, int row, float4 (&v)[kBatch], uint64_t policy) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      v[u] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       if (i < last) {
-        x = ldg_once4(unit_ptr(a, row, k));
+        v[u] = ldg_hint4(unit_ptr(a, row, k), policy);
         i += step;
         if (i < last) k.advance(step, a.per_slice);
       }
-      v[4 * u] = x.x;
-      v[4 * u + 1] = x.y;
-      v[4 * u + 2] = x.z;
-      v[4 * u + 3] = x.w;
     }
-    stats_add<ENT>(s, v, a.c);
   }
-  return s;
+};
+
+// A CTA's threads bring their sums together: each warp's into shared memory,
+// then warp 0 (after a barrier) adds them up.
+template <bool ENT>
+__device__ __forceinline__ void fast_warp_sums(const FastSums& s, float2* shared, int warp, int lane) {
+  const float z = warp_sum(s.z.x + s.z.y);
+  const float w = ENT ? warp_sum(s.w.x + s.w.y) : 0.0f;
+  if (lane == 0) shared[warp] = make_float2(z, w);
+}
+template <bool ENT, int WARPS>
+__device__ __forceinline__ PartStats fast_part(const float2* shared, int lane, float k) {
+  PartStats p{0.0, 0.0, k};
+  if (lane < WARPS) {
+    p.z = shared[lane].x;
+    p.w = shared[lane].y;
+  }
+#pragma unroll
+  for (int o = WARPS > 16 ? 16 : 8; o > 0; o >>= 1) {
+    p.z += __shfl_xor_sync(0xFFFFFFFFu, p.z, o);
+    if (ENT) p.w += __shfl_xor_sync(0xFFFFFFFFu, p.w, o);
+  }
+  p.w *= kLn2;
+  return p;
 }
 
-// Block-wide merge; every thread returns the result.  `shared` holds a slot per warp.
-template <bool ENT>
-__device__ __forceinline__ SoftmaxStats block_stats(SoftmaxStats s, SoftmaxStats* shared, ExpScale c) {
-  s = stats_warp<ENT>(s, c);
-  const int warps = static_cast<int>(blockDim.x) >> 5;
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = s;
-  __syncthreads();
-  s = shared[0];
-  for (int i = 1; i < warps; ++i) s = stats_merge<ENT>(s, shared[i], c);
-  __syncthreads();
-  return s;
+// The careful sums of units [first, last) by `warps` warps, whose first lane
+// leaves them in `shared`.
+__device__ __noinline__ void careful_warp_sums(const SliceArgs& a, int row, int first, int last, int thread,
+                                               int threads, CarefulSums* shared) {
+  UnitReader reader(a, first, last, thread, threads);
+  CarefulSums s = careful_empty();
+  const uint64_t policy = policy_evict_last();
+  while (reader.i < last) {
+    float4 v[kBatch];
+    reader.load(a, row, v, policy);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) careful_add(s, v[u], a.c);
+  }
+  __syncwarp();
+  const float m = warp_max(s.m);
+  if (s.m != m) careful_rebase(s, m, a.c);
+  s.z = warp_sum(s.z);
+  s.w = warp_sum(s.w);
+  if ((thread & 31) == 0) shared[thread >> 5] = s;
+}
+__device__ __forceinline__ PartStats careful_part(const CarefulSums* shared, int lane, int warps, const ExpScale& c) {
+  PartStats p{0.0, 0.0, -FLT_MAX};
+  if (lane < warps) {
+    p.z = shared[lane].z;
+    p.w = static_cast<double>(shared[lane].w) * c.inv_t;
+    p.ref = shared[lane].m;
+  }
+  return merge_parts<false, 32>(p, c);
+}
+
+// One CTA's part of a row, as the CTAs of a cluster exchange it.
+struct alignas(16) PartSlot {
+  double z, w;
+  float ref, pad[3];
+};
+__device__ __forceinline__ void send_part(PartSlot* slot, uint32_t rank, const PartStats& p) {
+  const uint32_t at = mapa(smem_u32(slot), rank);
+  st_dsmem_f64(at, p.z);
+  st_dsmem_f64(at + 8, p.w);
+  st_dsmem_u32(at + 16, __float_as_uint(p.ref));
+}
+__device__ __forceinline__ PartStats lane_part(const PartSlot* slots, int lane, int parts) {
+  PartStats p{0.0, 0.0, -FLT_MAX};
+  if (lane < parts) {
+    p.z = slots[lane].z;
+    p.w = slots[lane].w;
+    p.ref = slots[lane].ref;
+  }
+  return p;
 }
 
 __device__ __forceinline__ float token_logit(const SliceArgs& a, int row, int token) {
@@ -99,38 +146,41 @@ __device__ __forceinline__ float token_logit(const SliceArgs& a, int row, int to
   return a.slices[s][static_cast<size_t>(row) * a.V_s + (token - s * a.V_s)];
 }
 
-__device__ __forceinline__ void store_unit(float* p, const float (&g)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(g[0], g[1], g[2], g[3]);
+__device__ __forceinline__ void store_unit(float* p, const float4& g, uint64_t policy) {
+  stg_hint4(p, __float_as_uint(g.x), __float_as_uint(g.y), __float_as_uint(g.z), __float_as_uint(g.w), policy);
 }
-__device__ __forceinline__ void store_unit(__nv_bfloat16* p, const float (&g)[4]) {
+__device__ __forceinline__ void store_unit(__nv_bfloat16* p, const float4& g, uint64_t policy) {
   // one rounding to bf16 at the end: the next step is a bf16 matrix product
-  __nv_bfloat162 lo = __floats2bfloat162_rn(g[0], g[1]), hi = __floats2bfloat162_rn(g[2], g[3]);
-  uint2 v;
-  v.x = reinterpret_cast<uint32_t&>(lo);
-  v.y = reinterpret_cast<uint32_t&>(hi);
-  *reinterpret_cast<uint2*>(p) = v;
+  __nv_bfloat162 lo = __floats2bfloat162_rn(g.x, g.y), hi = __floats2bfloat162_rn(g.z, g.w);
+  stg_hint2(p, reinterpret_cast<uint32_t&>(lo), reinterpret_cast<uint32_t&>(hi), policy);
 }
 
-// A row's gradient coefficients (see the file's head).
+// A row's gradient coefficients for one CTA's exponentials (see the file's
+// head): G_j = e_j (alpha + gamma y_j) + at_token 1[j = token], where y_j is
+// what e_j is taken from: the exponent c l_j - ref of 2 (fast), or l_j - ref
+// (careful).
 struct GradCoef {
-  float m, alpha, gamma, at_token;
+  float ref, alpha, gamma, at_token;
   int token;  // -1: the row does not count, its gradient is 0
+  int careful;
 };
 
-__device__ __forceinline__ GradCoef grad_coef(double g, double h, double m, double z, double log_z, double entropy,
-                                              double temperature, int token) {
-  const double inv_t = 1.0 / temperature;
+// From df / dlogp = g and df / dH = h; `up`: the CTA's reference less the
+// row's (fast: an integer <= 0), ref: the CTA's reference.
+template <bool FAST>
+__device__ __forceinline__ GradCoef grad_coef(double g, double h, double z, double log_z, double entropy, double up,
+                                              float ref, const ExpScale& c, int token) {
   GradCoef k;
-  k.m = static_cast<float>(m);
-  k.gamma = 0.0f;
-  double alpha = -g * inv_t / z;
-  if (h != 0.0) {
-    alpha -= h * (entropy - log_z) * inv_t / z;
-    k.gamma = static_cast<float>(-h * inv_t * inv_t / z);
-  }
-  k.alpha = static_cast<float>(alpha);
-  k.at_token = static_cast<float>(g * inv_t);
+  k.ref = ref;
   k.token = token;
+  k.careful = !FAST;
+  // 1 / z of the exponentials as they are computed, relative to the CTA's reference
+  double f = kExpMean / z;
+  if (FAST) f *= exp2_int(up);
+  f *= -c.inv_t;
+  k.alpha = static_cast<float>(f * (h != 0.0 ? g + h * (entropy - log_z + up * kLn2) : g));
+  k.gamma = h != 0.0 ? static_cast<float>(f * h * (FAST ? kLn2 : c.inv_t)) : 0.0f;
+  k.at_token = static_cast<float>(g * c.inv_t);
   return k;
 }
 
@@ -138,30 +188,72 @@ struct GradArgs {
   void* grad[VSL_MAX_SLICES];
 };
 
-// Gradient of units [first, last) of a row by the whole CTA.
+__device__ __forceinline__ void add_at_token(const GradCoef& k, int i, float4& g) {
+  const int at = k.token - 4 * i;
+  if (at >= 0 && at < 4) {
+    if (at == 0) g.x += k.at_token;
+    if (at == 1) g.y += k.at_token;
+    if (at == 2) g.z += k.at_token;
+    if (at == 3) g.w += k.at_token;
+  }
+}
+
+// Gradient of one unit (the i-th of the row) from its logits.
+__device__ __forceinline__ float4 unit_grad(const float4& x, const GradCoef& k, const ExpScale& c, int i) {
+  const float v[4] = {x.x, x.y, x.z, x.w};
+  float g[4];
+  if (!k.careful) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float y = max_nan(__fmaf_rn(v[j], c.c, -k.ref), -200.0f);
+      g[j] = exp2_fast(y) * __fmaf_rn(k.gamma, y, k.alpha);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float t = v[j] - k.ref;
+      g[j] = exp_of(t, c) * __fmaf_rn(k.gamma, finite_low(t), k.alpha);
+    }
+  }
+  float4 r = make_float4(g[0], g[1], g[2], g[3]);
+  add_at_token(k, i, r);
+  return r;
+}
+
+// Gradient of units [first, last) of a row from global memory, a slice's run
+// at a time.
 template <typename T>
 __device__ __forceinline__ void part_grad(const SliceArgs& a, const GradArgs& out, const GradCoef& k, int row,
-                                          int first, int last) {
-  int i = first + static_cast<int>(threadIdx.x);
-  SliceCursor cur;
-  cur.start(i < last ? i : first, a.per_slice);
-  const int step = static_cast<int>(blockDim.x);
-  for (; i < last; i += step) {
-    T* dst = static_cast<T*>(out.grad[cur.slice]) + static_cast<size_t>(row) * a.V_s + 4 * static_cast<size_t>(cur.at);
-    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (k.token >= 0) {
-      // a plain load: the gradient may be written over the logits
-      const float4 x = *reinterpret_cast<const float4*>(unit_ptr(a, row, cur));
-      const float v[4] = {x.x, x.y, x.z, x.w};
+                                          int first, int last, int thread, int threads) {
+  SliceCursor run;
+  run.start(min(first, a.units - 1), a.per_slice);
+  const size_t row_at = static_cast<size_t>(row) * a.V_s;
+  const uint64_t once = policy_evict_first();
+  for (int u = first; u < last;) {
+    const int n = min(last - u, a.per_slice - run.at);
+    const size_t at = row_at + 4 * static_cast<size_t>(run.at);
+    const float* src = a.slices[run.slice] + at;
+    T* dst = static_cast<T*>(out.grad[run.slice]) + at;
+    for (int i = thread; i < n; i += kBatch * threads) {
+      float4 x[kBatch];
+      if (k.token >= 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float t = v[j] - k.m;
-        g[j] = exp_of(t, a.c) * __fmaf_rn(k.gamma, finite_low(t), k.alpha);
-        if (4 * i + j == k.token) g[j] += k.at_token;
+        for (int b = 0; b < kBatch; ++b)
+          if (i + b * threads < n) x[b] = ldg_hint4(src + 4 * (i + b * threads), once);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (i + b * threads < n) x[b] = unit_grad(x[b], k, a.c, u + i + b * threads);
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (i + b * threads < n) store_unit(dst + 4 * (i + b * threads), x[b], once);
     }
-    store_unit(dst, g);
-    if (i + step < last) cur.advance(step, a.per_slice);
+    u += n;
+    run.at = 0;
+    ++run.slice;
   }
 }
 
@@ -171,24 +263,91 @@ struct LogprobArgs {
   float* logprob;
   float* entropy;  // may be null
   float2* stats;   // may be null
+  int cluster;     // CTAs per row
+  int per_part;    // units per CTA
 };
 
+// A cluster per row: each CTA streams a part of the row once; the CTAs exchange
+// their sums over distributed shared memory.
 template <bool ENT>
 __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  __shared__ SoftmaxStats shared[kWarps];
-  const int row = static_cast<int>(blockIdx.x);
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float first_max[kWarps];
+  __shared__ float2 warps[kWarps];
+  __shared__ CarefulSums careful_warps[kWarps];
+  __shared__ PartSlot slots[2][kMaxCluster];
+  __shared__ int redo;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int row = static_cast<int>(blockIdx.x) / a.cluster;
   const int token = a.tokens[row];
-  const bool on = token >= 0 && token < 4 * a.in.units;
-  SoftmaxStats s{0.0f, 1.0f, 0.0f};
-  RowScore r{0.0, 0.0, 0.0};
-  if (on) {
-    s = block_stats<ENT>(part_stats<ENT>(a.in, row, 0, a.in.units), shared, a.in.c);
-    if (threadIdx.x == 0) r = row_score<ENT>(s, token_logit(a.in, row, token), a.in.temperature);
+  if (token < 0 || token >= 4 * a.in.units) {  // the whole cluster's: the row does not count
+    if (rank == 0 && threadIdx.x == 0) {
+      a.logprob[row] = 0.0f;
+      if (ENT) a.entropy[row] = 0.0f;
+      if (a.stats != nullptr) a.stats[row] = make_float2(0.0f, 1.0f);
+    }
+    return;
   }
-  if (threadIdx.x == 0) {
+  const float logit = warp == 0 ? token_logit(a.in, row, token) : 0.0f;
+  const int first = min(a.in.units, rank * a.per_part), last = min(a.in.units, first + a.per_part);
+  const uint64_t policy = policy_evict_first();
+  UnitReader reader(a.in, first, last, threadIdx.x, kThreads);
+  float4 v[kBatch];
+  reader.load(a.in, row, v, policy);
+  float m = -FLT_MAX;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) m = fmaxf(m, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
+  m = warp_max(m);
+  if (lane == 0) first_max[warp] = m;
+  __syncthreads();
+  const float k = fast_reference(warp_max(first_max[lane % kWarps]), a.in.c.c);
+  FastSums s{};
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+  while (reader.i < last) {
+    reader.load(a.in, row, v, policy);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+  }
+  fast_warp_sums<ENT>(s, warps, warp, lane);
+  __syncthreads();
+  if (warp == 0) {
+    const PartStats p = fast_part<ENT, kWarps>(warps, lane, k);
+    if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
+  }
+  cluster_sync();  // also: no CTA leaves while another may write to it
+  if (warp == 0) {
+    PartStats p = lane_part(slots[0], lane, a.cluster);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p));
+    p = merge_parts<true, kMaxCluster>(p, a.in.c);
+    ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
+    if (ok && rank == 0) {
+      const RowScore r = row_score<true, ENT>(p, logit, a.in.c);
+      if (lane == 0) {
+        a.logprob[row] = static_cast<float>(r.logprob);
+        if (ENT) a.entropy[row] = static_cast<float>(r.entropy);
+        if (a.stats != nullptr) a.stats[row] = make_float2(p.ref, static_cast<float>(r.z));
+      }
+    }
+    if (lane == 0) redo = !ok;
+  }
+  __syncthreads();
+  if (!redo) return;  // the cluster's CTAs agree: they saw the same sums
+  careful_warp_sums(a.in, row, first, last, threadIdx.x, kThreads, careful_warps);
+  __syncthreads();
+  if (warp == 0) {
+    const PartStats p = careful_part(careful_warps, lane, kWarps, a.in.c);
+    if (lane < a.cluster) send_part(&slots[1][rank], lane, p);
+  }
+  cluster_sync();
+  if (rank != 0 || warp != 0) return;
+  const PartStats p = merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c);
+  const RowScore r = row_score<false, ENT>(p, logit, a.in.c);
+  if (lane == 0) {
     a.logprob[row] = static_cast<float>(r.logprob);
     if (ENT) a.entropy[row] = static_cast<float>(r.entropy);
-    if (a.stats != nullptr) a.stats[row] = make_float2(s.m, s.z);
+    if (a.stats != nullptr) a.stats[row] = make_float2(p.ref, -static_cast<float>(r.z));  // the sign: careful
   }
 }
 
@@ -215,10 +374,11 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(const __g
   const double g = a.d_logprob[row], h = a.d_entropy != nullptr ? a.d_entropy[row] : 0.0f;
   if (token >= 0 && token < 4 * a.in.units && (g != 0.0 || h != 0.0)) {
     const float2 s = a.stats[row];
-    const double z = s.y > 0.0f ? s.y : NAN;
-    k = grad_coef(g, h, s.x, z, log(z), h != 0.0 ? a.entropy[row] : 0.0, a.in.temperature, token);
+    const double z = fabs(static_cast<double>(s.y)), ent = h != 0.0 ? a.entropy[row] : 0.0f;
+    k = s.y < 0.0f ? grad_coef<false>(g, h, z, log(z), ent, 0.0, s.x, a.in.c, token)
+                   : grad_coef<true>(g, h, z, log(z), ent, 0.0, s.x, a.in.c, token);
   }
-  part_grad<T>(a.in, a.out, k, row, first, last);
+  part_grad<T>(a.in, a.out, k, row, first, last, threadIdx.x, kThreads);
 }
 
 struct PolicyArgs {
@@ -235,26 +395,46 @@ struct PolicyArgs {
   float* entropy;  // may be null
   float clip_low, clip_high, kl_coef, entropy_coef;
   int grad;
+  int cluster;   // CTAs per row
+  int per_part;  // units per CTA
 };
 
-// The row's loss and outputs (one thread), and its gradient coefficients.
-__device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int token, const SoftmaxStats& s,
-                                               float logit, bool write) {
-  const RowScore r = row_score<true>(s, logit, a.in.temperature);
-  const double w = a.weights != nullptr ? a.weights[row] : 1.0f;
-  const double adv = a.advantages[row];
-  const double ratio = exp(r.logprob - static_cast<double>(a.old_logprob[row]));
+// A row's own inputs, read before its sums are ready.
+struct RowInputs {
+  float logit, old_logprob, ref_logprob, advantage, weight;
+};
+__device__ __forceinline__ RowInputs row_inputs(const PolicyArgs& a, int row, int token) {
+  RowInputs r;
+  // the token's logit, before any CTA may write the gradient over it
+  r.logit = token_logit(a.in, row, token);
+  r.old_logprob = a.old_logprob[row];
+  r.ref_logprob = a.ref_logprob != nullptr ? a.ref_logprob[row] : 0.0f;
+  r.advantage = a.advantages[row];
+  r.weight = a.weights != nullptr ? a.weights[row] : 1.0f;
+  return r;
+}
+
+// The row's loss and outputs, and the CTA's gradient coefficients, by one warp
+// (every lane holds p, the row's sums; ref is the CTA's reference).
+template <bool FAST, bool ENT>
+__device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int token, const RowInputs& in,
+                                               const PartStats& p, float ref, int lane, bool write) {
+  const RowScore r = row_score<FAST, ENT>(p, in.logit, a.in.c);
+  const double w = in.weight, adv = in.advantage;
+  const double d = static_cast<double>(in.ref_logprob) - r.logprob;
+  // exp(logprob - old) - 1 and exp(ref - logprob) - 1 side by side
+  const double em = expm1(lane == 1 ? d : r.logprob - static_cast<double>(in.old_logprob));
+  const double ratio = __shfl_sync(0xFFFFFFFFu, em, 0) + 1.0, em_d = __shfl_sync(0xFFFFFFFFu, em, 1);
   const double low = 1.0 - static_cast<double>(a.clip_low), high = 1.0 + static_cast<double>(a.clip_high);
   const double free_term = ratio * adv, clip_term = fmin(fmax(ratio, low), high) * adv;
   double loss = free_term != free_term ? NAN : -(free_term <= clip_term ? free_term : clip_term);
   double g = free_term != free_term ? NAN : free_term <= clip_term ? -adv * ratio : 0.0;
   double kl = 0.0;
   if (a.ref_logprob != nullptr) {
-    const double d = static_cast<double>(a.ref_logprob[row]) - r.logprob;
-    kl = d > 700.0 ? INFINITY : expm1(d) - d;  // not inf - inf
+    kl = d > 700.0 ? INFINITY : em_d - d;  // not inf - inf
     if (a.kl_coef != 0.0f) {
       loss += static_cast<double>(a.kl_coef) * kl;
-      g -= static_cast<double>(a.kl_coef) * expm1(d);
+      g -= static_cast<double>(a.kl_coef) * em_d;
     }
   }
   double h = 0.0;
@@ -262,37 +442,102 @@ __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int
     loss -= static_cast<double>(a.entropy_coef) * r.entropy;
     h = -w * static_cast<double>(a.entropy_coef);
   }
-  if (write) {
+  if (write && lane == 0) {
     a.loss[row] = static_cast<float>(w * loss);
     if (a.logprob != nullptr) a.logprob[row] = static_cast<float>(r.logprob);
     if (a.kl != nullptr) a.kl[row] = static_cast<float>(kl);
     if (a.entropy != nullptr) a.entropy[row] = static_cast<float>(r.entropy);
   }
-  const double z = s.z > 0.0f ? s.z : NAN;
-  return grad_coef(w * g, h, s.m, z, r.log_z, r.entropy, a.in.temperature, token);
+  const double up = FAST ? static_cast<double>(ref) - static_cast<double>(p.ref) : 0.0;
+  return grad_coef<FAST>(w * g, h, r.z, r.log_z, r.entropy, up, FAST ? ref : p.ref, a.in.c, token);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
-  __shared__ SoftmaxStats shared[kWarps];
+// A cluster per row.  Its CTAs stream the row once for the sums, exchange them
+// over distributed shared memory, and read their parts again for the gradient,
+// out of the L2 cache: the first reading asks it to keep the lines, the second
+// and the gradient's stores to let theirs go first.
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float first_max[kWarps];
+  __shared__ float2 warps[kWarps];
+  __shared__ CarefulSums careful_warps[kWarps];
+  __shared__ PartSlot slots[2][kMaxCluster];
   __shared__ GradCoef coef;
-  const int row = static_cast<int>(blockIdx.x);
+  __shared__ int redo;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int row = static_cast<int>(blockIdx.x) / a.cluster;
+  const int first = min(a.in.units, rank * a.per_part), last = min(a.in.units, first + a.per_part);
   const int token = a.tokens[row];
-  const bool on = token >= 0 && token < 4 * a.in.units && (a.weights == nullptr || a.weights[row] != 0.0f);
-  if (on) {
-    const SoftmaxStats s = block_stats<true>(part_stats<true>(a.in, row, 0, a.in.units), shared, a.in.c);
-    if (threadIdx.x == 0) coef = policy_row(a, row, token, s, token_logit(a.in, row, token), true);
-  } else if (threadIdx.x == 0) {
-    coef = GradCoef{};
-    coef.token = -1;
-    a.loss[row] = 0.0f;
-    if (a.logprob != nullptr) a.logprob[row] = 0.0f;
-    if (a.kl != nullptr) a.kl[row] = 0.0f;
-    if (a.entropy != nullptr) a.entropy[row] = 0.0f;
+  if (token < 0 || token >= 4 * a.in.units || (a.weights != nullptr && a.weights[row] == 0.0f)) {
+    if (rank == 0 && threadIdx.x == 0) {
+      a.loss[row] = 0.0f;
+      if (a.logprob != nullptr) a.logprob[row] = 0.0f;
+      if (a.kl != nullptr) a.kl[row] = 0.0f;
+      if (a.entropy != nullptr) a.entropy[row] = 0.0f;
+    }
+    GradCoef off{};
+    off.token = -1;
+    if (a.grad) part_grad<T>(a.in, a.out, off, row, first, last, threadIdx.x, kThreads);
+    return;
   }
-  if (!a.grad) return;
+  RowInputs in{};
+  if (warp == 0) in = row_inputs(a, row, token);
+  const uint64_t keep = policy_evict_last();
+  UnitReader reader(a.in, first, last, threadIdx.x, kThreads);
+  float4 v[kBatch];
+  reader.load(a.in, row, v, keep);
+  float m = -FLT_MAX;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) m = fmaxf(m, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
+  m = warp_max(m);
+  if (lane == 0) first_max[warp] = m;
   __syncthreads();
-  part_grad<T>(a.in, a.out, coef, row, 0, a.in.units);
+  const float k = fast_reference(warp_max(first_max[lane % kWarps]), a.in.c.c);
+  FastSums s{};
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+  while (reader.i < last) {
+    reader.load(a.in, row, v, keep);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+  }
+  fast_warp_sums<ENT>(s, warps, warp, lane);
+  __syncthreads();
+  if (warp == 0) {
+    const PartStats p = fast_part<ENT, kWarps>(warps, lane, k);
+    if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
+  }
+  cluster_sync();  // also: no CTA leaves while another may write to it
+  if (warp == 0) {
+    PartStats p = lane_part(slots[0], lane, a.cluster);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p));
+    p = merge_parts<true, kMaxCluster>(p, a.in.c);
+    ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
+    if (ok) {
+      const GradCoef g = policy_row<true, ENT>(a, row, token, in, p, k, lane, rank == 0);
+      if (lane == 0) coef = g;
+    }
+    if (lane == 0) redo = !ok;
+  }
+  __syncthreads();
+  if (redo) {  // the cluster's CTAs agree: they saw the same sums
+    careful_warp_sums(a.in, row, first, last, threadIdx.x, kThreads, careful_warps);
+    __syncthreads();
+    if (warp == 0) {
+      const PartStats p = careful_part(careful_warps, lane, kWarps, a.in.c);
+      if (lane < a.cluster) send_part(&slots[1][rank], lane, p);
+    }
+    cluster_sync();
+    if (warp == 0) {
+      const PartStats p = merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c);
+      const GradCoef g = policy_row<false, ENT>(a, row, token, in, p, p.ref, lane, rank == 0);
+      if (lane == 0) coef = g;
+    }
+    __syncthreads();
+  }
+  if (a.grad) part_grad<T>(a.in, a.out, coef, row, first, last, threadIdx.x, kThreads);
 }
 
 SliceArgs slice_args(const float* const* logits, int S, int V_s, float temperature) {
@@ -302,8 +547,70 @@ SliceArgs slice_args(const float* const* logits, int S, int V_s, float temperatu
   in.units = S * (V_s / 4);
   in.V_s = V_s;
   in.c = exp_scale(temperature);
-  in.temperature = temperature;
   return in;
+}
+
+// The SM count of the current device, read once per device.
+constexpr int kMaxDevices = 64;
+cudaError_t device_sms(int* sms) {
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t status[kMaxDevices];
+  static int count[kMaxDevices];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev],
+                 [&] { status[dev] = cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev); });
+  *sms = count[dev];
+  return status[dev];
+}
+
+// CTAs per row: as many as fill the SMs once (four to an SM), while a part
+// still has a unit or more per thread.
+cudaError_t row_cluster(int R, int units, int* cluster) {
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  int c = 1;
+  while (c < kMaxCluster && static_cast<long long>(R) * c < 4LL * sms && units / (2 * c) >= kThreads) c *= 2;
+  if (static_cast<long long>(R) * c > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  *cluster = c;
+  return cudaSuccess;
+}
+
+// CTAs per row of the policy kernel: at least so many that the rows being
+// worked on at a time (kPolicyCtas CTAs to an SM) take at most 72 MB, which
+// the L2 cache keeps until their second reading (2,048 rows of 151,936: 0.50
+// ms with 4 CTAs a row, 67 MB; 0.55 with 2; 0.60 with 8, whose exchanges cost
+// more than the cache gives); more while there are fewer CTAs than places.
+cudaError_t policy_cluster(int R, int units, int* cluster) {
+  int sms = 0;
+  const cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  int c = 1;
+  while (c < kMaxCluster && static_cast<long long>(kPolicyCtas) * sms / c * units * 16 > (72LL << 20)) c *= 2;
+  while (c < kMaxCluster && static_cast<long long>(R) * c < 1LL * kPolicyCtas * sms / 2 && units / (2 * c) >= kThreads) c *= 2;
+  if (static_cast<long long>(R) * c > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  *cluster = c;
+  return cudaSuccess;
+}
+
+template <typename Args>
+cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, int R, int cluster, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.gridDim = dim3(static_cast<unsigned>(R) * cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -317,11 +624,11 @@ cudaError_t launch_token_logprobs(const float* const* logits, int R, int S, int 
   a.logprob = logprob;
   a.entropy = entropy;
   a.stats = reinterpret_cast<float2*>(row_stats);
-  if (entropy != nullptr)
-    token_logprobs_kernel<true><<<R, kThreads, 0, stream>>>(a);
-  else
-    token_logprobs_kernel<false><<<R, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const cudaError_t e = row_cluster(R, a.in.units, &a.cluster);
+  if (e != cudaSuccess) return e;
+  a.per_part = (a.in.units + a.cluster - 1) / a.cluster;
+  return entropy != nullptr ? launch_clusters(token_logprobs_kernel<true>, a, R, a.cluster, stream)
+                            : launch_clusters(token_logprobs_kernel<false>, a, R, a.cluster, stream);
 }
 
 cudaError_t launch_token_logprobs_grad(const float* const* logits, int R, int S, int V_s, const int32_t* token_ids,
@@ -368,11 +675,15 @@ cudaError_t launch_policy_loss(const float* const* logits, int R, int S, int V_s
   a.clip_high = in.clip_high;
   a.kl_coef = in.kl_coef;
   a.entropy_coef = in.entropy_coef;
+  const cudaError_t e = policy_cluster(R, a.in.units, &a.cluster);
+  if (e != cudaSuccess) return e;
+  a.per_part = (a.in.units + a.cluster - 1) / a.cluster;
+  const bool ent = a.entropy != nullptr || a.entropy_coef != 0.0f;
   if (out.grad_type == VSL_GRAD_BF16)
-    policy_loss_kernel<__nv_bfloat16><<<R, kThreads, 0, stream>>>(a);
-  else
-    policy_loss_kernel<float><<<R, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+    return ent ? launch_clusters(policy_loss_kernel<__nv_bfloat16, true>, a, R, a.cluster, stream)
+               : launch_clusters(policy_loss_kernel<__nv_bfloat16, false>, a, R, a.cluster, stream);
+  return ent ? launch_clusters(policy_loss_kernel<float, true>, a, R, a.cluster, stream)
+             : launch_clusters(policy_loss_kernel<float, false>, a, R, a.cluster, stream);
 }
 
 }  // namespace vsl

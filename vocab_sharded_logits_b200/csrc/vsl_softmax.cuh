@@ -1,17 +1,27 @@
-// vsl_softmax.cuh - the running softmax statistics of a row of vocab-sliced
-// logits, shared by the kernels that score given tokens.
+// vsl_softmax.cuh - the softmax statistics of a row of vocab-sliced logits,
+// shared by the kernels that score given tokens.
 //
-// For a row of logits l_j at temperature T, x_j = l_j / T, one pass keeps
-//   m = max_j l_j,  z = sum_j exp((l_j - m) / T),  w = sum_j exp((l_j - m) / T) (l_j - m),
+// For a row of logits l_j at temperature T one pass gives, with e_j =
+// exp((l_j - m) / T) for some reference m,
+//   z = sum_j e_j,   and where the entropy is asked for   w = sum_j e_j (l_j - m) / T,
 // from which, for a token t,
-//   log p_t = (l_t - m) / T - log z,     H = log z - w / (z T)  (the entropy).
-// exp((l - m) / T) is 2^(c (l - m)) with c = log2(e) / T.  c is carried as a
-// sum of two floats, hi <= c and lo > 0: the rounding of a single float c would
-// put the same relative error, |l - m| / T times 2^-24, on every far term of z.
-// Both parts are positive, so l = -inf gives -inf and an exponential of 0, and
-// a NaN stays one.  m starts at the lowest finite value, so l - m is never
-// inf - inf unless a logit is +inf, which makes z a NaN like a NaN logit does;
-// z = 0 means that every logit is -inf.
+//   log p_t = (l_t - m) / T - log z,     H = log z - w / z.
+//
+// The fast form.  e_j = 2^(c l_j - k) with c = log2(e) / T in float32 and k an
+// integer, so a logit costs one fused multiply-add, one ex2 and one addition
+// (and a bound and another multiply-add for w): no running maximum is kept.
+// k is taken from the largest of the first logits each thread of the CTA
+// reads: near the row's maximum, and the same for the whole CTA, so sums add
+// up as they are; the CTAs' different k are powers of two apart, which costs
+// no rounding.  What it rests on is checked afterwards: a row whose sums left
+// [2^-40, 2^60] (a NaN or +inf logit; none above -inf; logits some 30 T above
+// the first ones read, or all of them some 28 T below 0) or whose k exceeds
+// 2^20 is done again in the careful form.  c's rounding is a temperature off by at
+// most 2^-24, used consistently: log p_t moves by 2^-24 of its size at most,
+// and with w at hand the first-order term is taken out.
+//
+// The careful form keeps each thread's running maximum, e_j = exp((l_j - m) /
+// T) with c as a sum of two floats, and rescales when the maximum grows.
 #pragma once
 
 #include <cfloat>
@@ -23,101 +33,232 @@
 
 namespace vsl {
 
-// c = log2(e) / T as hi + lo, hi <= c, lo > 0.
+constexpr double kLn2 = 0.69314718055994530941723212145818;
+
+// log2(e) / T: nearest float (fast form), and as hi + lo with hi <= c, lo > 0
+// (careful form: both positive, so l = -inf gives -inf).
 struct ExpScale {
-  float hi, lo;
+  float c, hi, lo;
+  double inv_t;      // 1 / T
+  double inv_t_fast; // 1 / T as c has it: c ln 2
 };
 
 inline ExpScale exp_scale(float temperature) {
   const double c = 1.4426950408889634073599246810019 / static_cast<double>(temperature);
   ExpScale r;
-  r.hi = static_cast<float>(c);
+  r.c = static_cast<float>(c);
+  r.hi = r.c;
   if (static_cast<double>(r.hi) > c) r.hi = std::nextafterf(r.hi, 0.0f);
   r.lo = static_cast<float>(c - static_cast<double>(r.hi));
   if (!(r.lo > 0.0f)) r.lo = FLT_MIN;
+  r.inv_t = 1.0 / static_cast<double>(temperature);
+  r.inv_t_fast = static_cast<double>(r.c) * kLn2;
   return r;
 }
+
+// ex2.approx is off by at most 1.43e-7 relative on this part and, over a
+// binade, by -5.16e-8 in the mean (measured on 2^18 arguments in each of 30
+// binades; the errors repeat from one to the next).  A sum of many
+// exponentials keeps the mean error, so it is taken out of z, w and p.
+constexpr double kExpMean = 1.0 + 5.16e-8;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// exp(t / T) for t <= 0 (0 for -inf, NaN for NaN).
-__device__ __forceinline__ float exp_of(float t, ExpScale c) { return exp2_fast(__fmaf_rn(t, c.hi, t * c.lo)); }
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// two float32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// ------------------------------------------------------------------ fast form
+
+// A thread's sums: z, and w in units of log2 (sum of e times its exponent), as
+// two float32 partial sums each.
+struct FastSums {
+  float2 z, w;
+};
+
+// The CTA's k from the largest of the logits its threads read first.  Far
+// below 0 these are masked ones, as a rule: what follows is likely near 0.
+__device__ __forceinline__ float fast_reference(float top, float c) {
+  const float k = rintf(top * c);
+  return k < -30.0f ? 0.0f : k;
+}
+constexpr float kFastMaxK = 1048576.0f;
+
+// Four logits; their exponentials are returned.
+template <bool ENT>
+__device__ __forceinline__ float4 fast_add(FastSums& s, const float4& x, float c, float k) {
+  const float2 cc = make_float2(c, c), kk = make_float2(-k, -k);
+  float2 y0 = fma2(make_float2(x.x, x.y), cc, kk), y1 = fma2(make_float2(x.z, x.w), cc, kk);
+  if (ENT) {  // an exponential of 0 times a bounded exponent is 0
+    y0 = make_float2(max_nan(y0.x, -200.0f), max_nan(y0.y, -200.0f));
+    y1 = make_float2(max_nan(y1.x, -200.0f), max_nan(y1.y, -200.0f));
+  }
+  const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
+  s.z = add2(s.z, add2(e0, e1));
+  if (ENT) s.w = fma2(e1, y1, fma2(e0, y0, s.w));
+  return make_float4(e0.x, e0.y, e1.x, e1.y);
+}
+
+// ------------------------------------------------------------------ careful form
+
+// exp(t / T) (0 for -inf, NaN for NaN).
+__device__ __forceinline__ float exp_of(float t, const ExpScale& c) {
+  return exp2_fast(__fmaf_rn(t, c.hi, t * c.lo));
+}
 // t bounded from below, so that its product with an exponential of 0 is 0: at
 // -1e18 the exponential is 0 for every T up to 1e6, and a factor of up to 1e20
 // (a sum of exponentials, a gradient's coefficient) still gives a finite value.
 __device__ __forceinline__ float finite_low(float t) { return fmaxf(t, -1e18f); }
 
-struct SoftmaxStats {
+// A thread's sums relative to its running maximum m (w in units of l).  m
+// starts at the lowest finite value, so l - m is never inf - inf unless a
+// logit is +inf, which makes z a NaN like a NaN logit does; z = 0 means that
+// every logit is -inf.
+struct CarefulSums {
   float m, z, w;
 };
+__device__ __forceinline__ CarefulSums careful_empty() { return {-FLT_MAX, 0.0f, 0.0f}; }
 
-__device__ __forceinline__ SoftmaxStats stats_empty() { return {-FLT_MAX, 0.0f, 0.0f}; }
-
-// The statistics of two disjoint parts of a row.  ENT: w is kept.
-template <bool ENT>
-__device__ __forceinline__ SoftmaxStats stats_merge(const SoftmaxStats& a, const SoftmaxStats& b, ExpScale c) {
-  SoftmaxStats r;
-  r.m = fmaxf(a.m, b.m);
-  const float da = finite_low(a.m - r.m), db = finite_low(b.m - r.m);
-  const float fa = exp_of(da, c), fb = exp_of(db, c);
-  r.z = a.z * fa + b.z * fb;
-  r.w = 0.0f;
-  if (ENT) r.w = (a.w + da * a.z) * fa + (b.w + db * b.z) * fb;
-  return r;
+__device__ __forceinline__ void careful_rebase(CarefulSums& s, float m, const ExpScale& c) {
+  const float d = finite_low(s.m - m);
+  const float f = exp_of(d, c);
+  s.w = (s.w + d * s.z) * f;
+  s.z *= f;
+  s.m = m;
 }
-
-// Adds N logits to a thread's statistics: their maximum first (one rescaling
-// when it grows), then the exponentials.
-template <bool ENT, int N>
-__device__ __forceinline__ void stats_add(SoftmaxStats& s, const float (&v)[N], ExpScale c) {
-  float m = v[0];
+__device__ __forceinline__ void careful_add(CarefulSums& s, const float4& x, const ExpScale& c) {
+  const float v[4] = {x.x, x.y, x.z, x.w};
+  const float m = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+  if (m > s.m) careful_rebase(s, m, c);
 #pragma unroll
-  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
-  if (m > s.m) {
-    const float d = finite_low(s.m - m);
-    const float f = exp_of(d, c);
-    if (ENT) s.w = (s.w + d * s.z) * f;
-    s.z *= f;
-    s.m = m;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const float t = v[i] - s.m;
     const float e = exp_of(t, c);
     s.z += e;
-    if (ENT) s.w = __fmaf_rn(e, finite_low(t), s.w);
+    s.w = __fmaf_rn(e, finite_low(t), s.w);
   }
 }
 
-template <bool ENT>
-__device__ __forceinline__ SoftmaxStats stats_warp(SoftmaxStats s, ExpScale c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    SoftmaxStats b;
-    b.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, o);
-    b.z = __shfl_xor_sync(0xFFFFFFFFu, s.z, o);
-    b.w = ENT ? __shfl_xor_sync(0xFFFFFFFFu, s.w, o) : 0.0f;
-    s = stats_merge<ENT>(s, b, c);
-  }
-  return s;
+// ------------------------------------------------------------------ parts of a row
+
+// A CTA's part of a row, or the row: z and w (w in units of (l - m) / T)
+// relative to a reference: 2^(c l - ref) (fast) or exp((l - ref) / T) (careful).
+struct PartStats {
+  double z, w;
+  float ref;
+};
+
+// 2^n for an integer n <= 0 (0 below -1000).
+__device__ __forceinline__ double exp2_int(double n) {
+  return n < -1000.0 ? 0.0 : __hiloint2double((1023 + static_cast<int>(n)) << 20, 0);
 }
+
+// The parts in lanes 0 .. N - 1 (an empty one: z = w = 0, ref the lowest
+// value), brought to the largest reference; lanes 0 .. N - 1 hold the result.
+// FAST: the references are exponents of 2.
+template <bool FAST, int N>
+__device__ __forceinline__ PartStats merge_parts(PartStats p, const ExpScale& c) {
+  float ref = p.ref;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
+  double d = static_cast<double>(p.ref) - static_cast<double>(ref);  // <= 0 (NaN: both infinite)
+  double f = 0.0;
+  if (FAST) {
+    if (d > -1000.0) {
+      f = exp2_int(d);
+      d *= kLn2;
+    } else {
+      d = 0.0;  // a far lower part adds 0
+    }
+  } else {
+    d *= c.inv_t;
+    if (d > -1000.0) {
+      f = exp(d);
+    } else {
+      d = 0.0;
+    }
+  }
+  p.w = (p.w + d * p.z) * f;
+  p.z *= f;
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    p.z += __shfl_xor_sync(0xFFFFFFFFu, p.z, o);
+    p.w += __shfl_xor_sync(0xFFFFFFFFu, p.w, o);
+  }
+  p.ref = ref;
+  return p;
+}
+
+// Whether a CTA's fast sums hold (a row's, when its parts' do and it is not
+// below kFastLeast).
+__device__ __forceinline__ bool fast_holds(const PartStats& p) { return p.z <= 0x1p60 && fabsf(p.ref) <= kFastMaxK; }
+constexpr double kFastLeast = 0x1p-40;
 
 // A row's results in 64 bits (a difference of two logprobs, a ratio near a
 // border and the KL estimate near 0 all lose digits in 32).
 struct RowScore {
-  double logprob, log_z, entropy;
+  double logprob, z, log_z, entropy;
 };
-template <bool ENT>
-__device__ __forceinline__ RowScore row_score(const SoftmaxStats& s, float token_logit, float temperature) {
+template <bool FAST, bool ENT>
+__device__ __forceinline__ RowScore row_score(const PartStats& s, float token_logit, const ExpScale& c) {
   RowScore r;
-  const double inv_t = 1.0 / static_cast<double>(temperature);
-  const double z = s.z > 0.0f ? static_cast<double>(s.z) : static_cast<double>(NAN);  // all -inf, NaN or +inf
-  r.log_z = log(z);
-  r.logprob = (static_cast<double>(token_logit) - static_cast<double>(s.m)) * inv_t - r.log_z;
-  r.entropy = ENT ? r.log_z - static_cast<double>(s.w) / z * inv_t : 0.0;
+  // 0: every logit is -inf; NaN: a NaN or +inf logit
+  r.z = s.z > 0.0 ? s.z * kExpMean : static_cast<double>(NAN);
+  r.log_z = log(r.z);
+  const double l = token_logit, ref = s.ref;
+  const double x = FAST ? l * c.inv_t_fast - ref * kLn2 : (l - ref) * c.inv_t;
+  r.logprob = x - r.log_z;
+  r.entropy = 0.0;
+  if (ENT) {
+    const double mean = s.w * kExpMean / r.z;  // of x under p
+    r.entropy = r.log_z - mean;
+    // the temperature that c has, to first order
+    if (FAST && x > -1e30) r.logprob += (c.inv_t / c.inv_t_fast - 1.0) * (x - mean);
+    if (r.entropy < 0.0) r.entropy = 0.0;
+  }
+  if (r.logprob > 0.0) r.logprob = 0.0;
   return r;
 }
 
