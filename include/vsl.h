@@ -322,8 +322,8 @@ VSL_API vsl_status vsl_verify_drafts(const int32_t* token_ids, const float* toke
  * blog): upstream's flag rejects LoRA; here the rows of one batch may each use
  * an adapter of their own. */
 
-/* Bytes of device workspace vsl_adapters_add needs (0 for non-positive sizes). */
-VSL_API size_t vsl_adapters_workspace_bytes(int32_t R, int32_t rank);
+/* Bytes of device workspace vsl_adapters_add needs (0 for sizes it rejects). */
+VSL_API size_t vsl_adapters_workspace_bytes(int32_t R, int32_t n_adapters, int32_t rank);
 
 /* vsl_adapters_add - adds each row's low-rank term to the base logits:
  *   u[r][k]         = scale[a] * sum_h hidden[r][h] * A[a][k][h],  a = adapter_ids[r]
@@ -346,7 +346,7 @@ VSL_API size_t vsl_adapters_workspace_bytes(int32_t R, int32_t rank);
  *   tile_stats    : (optional, NULL) the tile statistics of out_slices, as
  *                   vsl_tile_stats writes them, 32-byte aligned.
  *   workspace     : device, 16-byte aligned, workspace_bytes >=
- *                   vsl_adapters_workspace_bytes(R, rank); its contents are
+ *                   vsl_adapters_workspace_bytes(R, n_adapters, rank); its contents are
  *                   written and read by this call's kernels only.  Calls that
  *                   can run at the same time (two streams, or two captured
  *                   graphs) need a workspace each.

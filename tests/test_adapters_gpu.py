@@ -144,7 +144,7 @@ def test_repeatable_streams_graphs_and_workspaces(cuda_device):
     want = [vsl.adapters_add(l, h, a, b, i, scale=s) for h, l, a, b, s, i in cases]
     again = [vsl.adapters_add(l, h, a, b, i, scale=s) for h, l, a, b, s, i in cases]
     graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
-    spaces = [torch.empty(vsl.adapters_workspace_bytes(40, 16), dtype=torch.uint8, device=cuda_device) for _ in cases]
+    spaces = [torch.empty(vsl.adapters_workspace_bytes(40, 8, 16), dtype=torch.uint8, device=cuda_device) for _ in cases]
     torch.cuda.synchronize()
     for (h, l, a, b, s, i), ws, stream in zip(cases, spaces, streams):
         graph = torch.cuda.CUDAGraph()

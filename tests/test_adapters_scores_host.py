@@ -8,6 +8,7 @@ import vocab_sharded_logits_b200 as v
 
 INVALID, ALIGN, UNSUPPORTED, WORKSPACE = 1, 2, 3, 4
 vp = ctypes.c_void_p
+WS = v.adapters_workspace_bytes(4, 2, 8)
 FAKE = 0x10000                      # never dereferenced: validation fails first
 
 
@@ -17,14 +18,16 @@ def _arr(*addr):
 
 def _adapters(**kw):
     a = dict(logits=_arr(0x10000), out=_arr(0x20000), hidden=FAKE, R=4, H=64, S=1, V_s=512, a=FAKE, b=_arr(0x30000),
-             scale=None, n=2, rank=8, ids=FAKE, stats=None, ws=FAKE, ws_bytes=4 * 3 * 16 * 2, stream=None)
+             scale=None, n=2, rank=8, ids=FAKE, stats=None, ws=FAKE, ws_bytes=WS, stream=None)
     a.update(kw)
     return v.lib.vsl_adapters_add(*a.values())
 
 
 def test_adapters_refusals():
-    assert v.lib.vsl_adapters_workspace_bytes(4, 8) == 4 * 3 * 16 * 2       # rank padded to 16, three bf16 terms
-    assert v.lib.vsl_adapters_workspace_bytes(0, 8) == 0 and v.lib.vsl_adapters_workspace_bytes(4, -1) == 0
+    # 3 units (2 adapters and none) of 20 words in the plan, three terms of 16 x 16 bf16 each
+    assert WS == (4 + 3 * 20) * 4 + 3 * 3 * 16 * 16 * 2
+    for bad in ((0, 2, 8), (4, 0, 8), (4, 2, -1), (4, 2, 264)):
+        assert v.adapters_workspace_bytes(*bad) == 0
     for name in ("logits", "out", "hidden", "a", "b", "ids", "ws"):
         assert _adapters(**{name: None}) == INVALID, name
     for name in ("R", "H", "S", "V_s", "n", "rank"):
@@ -39,7 +42,7 @@ def test_adapters_refusals():
         assert _adapters(**{name: 0x10008}) == ALIGN, name
     assert _adapters(logits=_arr(0x10004)) == ALIGN and _adapters(out=_arr(0x20004)) == ALIGN
     assert _adapters(b=_arr(0x30008)) == ALIGN and _adapters(stats=0x40010) == ALIGN
-    assert _adapters(ws_bytes=4 * 3 * 16 * 2 - 1) == WORKSPACE
+    assert _adapters(ws_bytes=WS - 1) == WORKSPACE
     two = dict(S=2, logits=_arr(0x10000, 0x20000), b=_arr(0x30000, 0x40000))
     assert _adapters(**two, out=_arr(0x20000, 0x50000)) == INVALID          # another slice's logits
     assert _adapters(**two, out=_arr(0x50000, 0x50000)) == INVALID          # one output twice

@@ -96,7 +96,7 @@ def _load():
     l.vsl_verify_drafts.argtypes = [vp, vp, vp, i32, i32, vp, vp, vp, vp]
     f32 = ctypes.c_float
     l.vsl_adapters_workspace_bytes.restype = sz
-    l.vsl_adapters_workspace_bytes.argtypes = [i32, i32]
+    l.vsl_adapters_workspace_bytes.argtypes = [i32, i32, i32]
     l.vsl_adapters_add.restype = ctypes.c_int
     l.vsl_adapters_add.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), vp, i32, i32, i32, i32, vp,
                                    ctypes.POINTER(vp), vp, i32, i32, vp, vp, vp, sz, vp]
@@ -398,9 +398,9 @@ def _grad_slices(grad, grad_dtype, R, S, V_s, dev):
     return grad, 1 if dtype == torch.bfloat16 else 0
 
 
-def adapters_workspace_bytes(R, rank):
+def adapters_workspace_bytes(R, n_adapters, rank):
     """Bytes of device workspace one ``adapters_add`` call needs."""
-    return lib.vsl_adapters_workspace_bytes(int(R), int(rank))
+    return lib.vsl_adapters_workspace_bytes(int(R), int(n_adapters), int(rank))
 
 
 def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, out=None, stream=None, tile_stats=None,
@@ -413,7 +413,7 @@ def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, ou
     (None: 1).  rank is a multiple of 8 up to MAX_RANK.  ``out`` may be ``logits_slices`` (in place).
     With ``tile_stats`` (True, or a tensor to fill) the tile statistics of the result are written
     too, and the call returns ``(slices, stats)``.  workspace: a uint8 tensor of
-    ``adapters_workspace_bytes(R, rank)`` bytes (None: allocated for the call); calls that may run
+    ``adapters_workspace_bytes(R, n, rank)`` bytes (None: allocated for the call); calls that may run
     at the same time need one each.
     """
     R, S, V_s, dev = _slices(logits_slices, "adapters_add")
@@ -439,7 +439,7 @@ def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, ou
         if workspace is None:
             # from the pool of the stream that uses it
             with torch.cuda.stream(stream):
-                workspace = torch.empty(adapters_workspace_bytes(R, rank), dtype=torch.uint8, device=dev)
+                workspace = torch.empty(lib.vsl_adapters_workspace_bytes(R, n, rank), dtype=torch.uint8, device=dev)
         elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
             raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
         status = lib.vsl_adapters_add(_ptr_array(logits_slices), _ptr_array(out), _ptr(hidden), R, H, S, V_s, _ptr(a),

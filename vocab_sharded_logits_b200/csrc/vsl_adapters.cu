@@ -5,14 +5,16 @@
 // request uses adapter a adds its own low-rank term:
 //   u[r][k]        = scale[a] sum_h hidden[r][h] A[a][k][h],
 //   out_s[r][j]    = logits_s[r][j] + sum_k B_s[a][j][k] u[r][k].
-// Two kernels: u first (a few hundred KB), then one pass over the logits.
-//
-// Both products run on the tensor cores with bf16 operands and fp32 sums over
-// groups of 16 rows: for each adapter that occurs in a group the product is
-// taken for all 16 rows, and each row keeps the result of its own adapter (a
-// selection, not a multiplication by 0, so that one request's infinities or
-// NaNs never reach another's row).  u is not rounded to bf16: it is carried as
-// three bf16 terms (8 + 8 + 8 bits), each multiplied with B.
+// Two kernels.  The first sorts the rows of a tile of 256 by adapter and forms
+// units: up to 16 rows of one adapter (or of none); it computes u of each unit
+// and leaves the units' rows behind as a plan.  The second passes over the
+// logits, a warp to a unit and 128 ids.  Both products run on the tensor cores
+// (mma.sync: the 16 rows of a unit are its M, and what bounds the work is the
+// logits' and the B's bytes) with bf16 operands and fp32 sums.  A unit's rows
+// share one adapter, so no row ever meets another adapter's numbers: one
+// request's infinities or NaNs never reach another's row, and no product is
+// computed to be thrown away.  u is not rounded to bf16: it is carried as three
+// bf16 terms (8 + 8 + 8 bits), each multiplied with B.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,14 +27,30 @@ namespace vsl {
 
 namespace {
 
-constexpr int kGroup = 16;        // rows per tensor-core product
-constexpr int kShrinkWarps = 8;
+constexpr int kUnitRows = 16;     // rows per tensor-core product
+constexpr int kTile = 256;        // rows sorted together
+constexpr int kShrinkWarps = 8;   // kShrinkWarps * 32 == kTile: a thread sorts a row
 constexpr int kExpandWarps = 4;
 constexpr int kTerms = 3;         // bf16 terms of u
+constexpr int kFragment = 32 * 4; // 32-bit registers of one A operand (16 x 16 bf16) over a warp
+constexpr int kMaxSplit = 4;      // CTAs that share H
 
-__host__ __device__ constexpr int padded_rank(int rank) { return (rank + 15) / 16 * 16; }
+__host__ __device__ constexpr int rank_steps(int rank) { return (rank + 15) / 16; }
+// Units a tile of `rows` rows over n adapters can have: full ones, a ragged one
+// per adapter and one of rows without an adapter.
+__host__ __device__ constexpr int unit_slots(int rows, int n) {
+  const int distinct = n < rows ? n + 1 : rows;
+  return rows / kUnitRows + distinct < rows ? rows / kUnitRows + distinct : rows;
+}
 
-// D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, fp32 sums.
+// The plan of a tile: its units' number, then a unit's adapter (-1: none) and
+// rows (-1: none) each.
+constexpr int kPlanUnit = 1 + kUnitRows;
+__host__ __device__ constexpr size_t plan_ints(int slots) { return 4 + static_cast<size_t>(slots) * (kPlanUnit + 3); }
+__device__ __forceinline__ int32_t* plan_unit(int32_t* plan, int slot) { return plan + 4 + slot * (kPlanUnit + 3); }
+
+// D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, fp32 sums.  Every lane of
+// the warp takes part.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -42,56 +60,100 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The adapter of row r (-1: none, or an id outside the pool).
-__device__ __forceinline__ int adapter_of(const int32_t* ids, int r, int R, int n) {
-  const int a = r < R ? ids[r] : -1;
-  return a >= 0 && a < n ? a : -1;
-}
-
 struct ShrinkArgs {
   const __nv_bfloat16* hidden;
   const __nv_bfloat16* a;
   const float* scale;  // may be null: 1
   const int32_t* ids;
-  __nv_bfloat16* u;    // [R][kTerms][padded rank]
-  int R, H, n, rank;
+  int32_t* plan;       // [tiles][plan_ints(slots)]
+  uint32_t* u;         // [tiles][slots][steps][kTerms][kFragment]: as the second kernel's lanes hold it
+  int R, H, n, rank, slots, split;
 };
 
-// u of the rows of one group that use its blockIdx.y-th adapter, ranks 16
-// blockIdx.z ..: the warps split H.
+// CTA (tile, unit, 16 ranks x a part of H): the warps split the part, the CTAs
+// of a cluster share H.
 __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(const __grid_constant__ ShrinkArgs p) {
-  __shared__ float part[kShrinkWarps][kGroup][16];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int row0 = static_cast<int>(blockIdx.x) * kGroup;
-  const int mine = adapter_of(p.ids, row0 + (lane & 15), p.R, p.n);
-  uint32_t left = __ballot_sync(0xFFFFFFFFu, mine >= 0) & 0xFFFFu, rows = 0;
-  int adapter = -1;
-  for (int i = 0; i <= static_cast<int>(blockIdx.y) && left; ++i) {
-    adapter = __shfl_sync(0xFFFFFFFFu, mine, __ffs(left) - 1);
-    rows = __ballot_sync(0xFFFFFFFFu, mine == adapter) & 0xFFFFu;
-    left &= ~rows;
-    if (i < static_cast<int>(blockIdx.y)) rows = 0;
+  __shared__ int key[kTile];
+  __shared__ int order[kTile];        // sorted position -> row of the tile
+  __shared__ int within[kTile];       // sorted position -> rows of its adapter before it
+  __shared__ int starts[kTile + 1];   // unit -> its first sorted position
+  __shared__ int warp_units[kShrinkWarps];
+  __shared__ float part[kShrinkWarps][kUnitRows][16];
+  __shared__ float parts[kMaxSplit][kUnitRows][16];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int slot = static_cast<int>(blockIdx.y), tile = static_cast<int>(blockIdx.x);
+  const int split_rank = static_cast<int>(cluster_ctarank());
+  const int k0 = static_cast<int>(blockIdx.z) / p.split * 16;
+  const int row0 = tile * kTile, rows = min(kTile, p.R - row0);
+
+  // ---- sort: rows by (adapter, row), those without an adapter last
+  int mine = 0x7FFFFFFF;  // past the tile's end
+  if (tid < rows) {
+    mine = p.ids[row0 + tid];
+    if (mine < 0 || mine >= p.n) mine = p.n;
   }
-  if (rows == 0) return;  // the group has fewer adapters
-  const int k0 = static_cast<int>(blockIdx.z) * 16;
-  const bool row_ok[2] = {((rows >> g) & 1u) != 0, ((rows >> (g + 8)) & 1u) != 0};
+  key[tid] = mine;
+  __syncthreads();
+  int before = 0, same = 0;  // rows of smaller adapters; rows of mine before me
+  for (int j = 0; j < rows; ++j) {
+    const int other = key[j];
+    before += other < mine;
+    same += (other == mine) & (j < tid);
+  }
+  const int at = before + same;
+  if (tid < rows) {
+    order[at] = tid;
+    within[at] = same;
+  }
+  __syncthreads();
+  // a unit starts at every 16th row of an adapter; its number: the starts before it
+  const bool begins = tid < rows && within[tid] % kUnitRows == 0;
+  const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, begins);
+  if (lane == 0) warp_units[warp] = __popc(ballot);
+  __syncthreads();
+  int unit = __popc(ballot & ((1u << lane) - 1u));
+  int units = 0;
+  for (int w = 0; w < kShrinkWarps; ++w) {
+    if (w < warp) unit += warp_units[w];
+    units += warp_units[w];
+  }
+  if (begins) starts[unit] = tid;
+  if (tid == 0) starts[units] = rows;
+  __syncthreads();
+  if (slot >= units) return;  // the whole cluster's
+  const int first = starts[slot], count = starts[slot + 1] - first;
+  const int adapter = key[order[first]] < p.n ? key[order[first]] : -1;
+
+  // ---- the plan, by the first CTA of the unit
+  if (blockIdx.z == 0) {
+    int32_t* plan = p.plan + tile * plan_ints(p.slots);
+    if (slot == 0 && tid == 0) plan[0] = units;
+    int32_t* entry = plan_unit(plan, slot);
+    if (tid < kUnitRows) entry[4 + tid] = tid < count ? row0 + order[first + tid] : -1;
+    if (tid == kUnitRows) entry[0] = adapter;
+  }
+  if (adapter < 0) return;
+
+  // ---- u of the unit: 16 rows x 16 ranks
+  const int g = lane >> 2, t = lane & 3;
+  const bool row_ok[2] = {g < count, g + 8 < count};
   const bool rank_ok[2] = {k0 + g < p.rank, k0 + 8 + g < p.rank};
   const __nv_bfloat16* h_row[2];
   const __nv_bfloat16* a_row[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    h_row[i] = p.hidden + static_cast<size_t>(row_ok[i] ? row0 + g + 8 * i : row0) * p.H;
+    h_row[i] = p.hidden + static_cast<size_t>(row0 + order[first + (row_ok[i] ? g + 8 * i : 0)]) * p.H;
     a_row[i] = p.a + (static_cast<size_t>(adapter) * p.rank + (rank_ok[i] ? k0 + 8 * i + g : 0)) * p.H;
   }
   float d[2][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // 32 columns of H a step: a lane's 8 consecutive ones serve two products
-  // (the order of the summed index is free, the same on both sides)
-  // (the loop's bound is the warp's, not the lane's: every lane takes part in
-  // a product, with zeros past the end of H)
+  // (the order of the summed index is free, the same on both sides).  The
+  // loop's bound is the warp's, not the lane's: every lane takes part in a
+  // product, with zeros past the end of H.
 #pragma unroll 4
-  for (int h0 = warp * 32; h0 < p.H; h0 += kShrinkWarps * 32) {
+  for (int h0 = (split_rank * kShrinkWarps + warp) * 32; h0 < p.H; h0 += p.split * kShrinkWarps * 32) {
     const int h = h0 + 8 * t;
     const bool in = h < p.H;
     uint4 x[2], y[2];
@@ -114,18 +176,27 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
     part[warp][g + 8][8 * i + 2 * t + 1] = d[i][3];
   }
   __syncthreads();
-  const int r = threadIdx.x >> 4, k = threadIdx.x & 15;
-  if (!((rows >> r) & 1u)) return;
+  const int r = tid >> 4, k = tid & 15;
   float u = 0.0f;
 #pragma unroll
   for (int w = 0; w < kShrinkWarps; ++w) u += part[w][r][k];
+  *cluster_ptr(&parts[split_rank][r][k], 0) = u;
+  cluster_sync();  // no access to another CTA's memory follows
+  if (split_rank != 0) return;
+  u = parts[0][r][k];
+  for (int c = 1; c < p.split; ++c) u += parts[c][r][k];
   if (p.scale != nullptr) u *= p.scale[adapter];
-  const int rp = padded_rank(p.rank);
-  __nv_bfloat16* out = p.u + static_cast<size_t>(row0 + r) * kTerms * rp + k0 + k;
+  // the second kernel's A operand: register i of lane 4 (r mod 8) + k / 4 holds the ranks of one row whose
+  // position in it, 2 * (k mod 4 / 2) .., its lanes' B take as well: ranks 4 t .. 4 t + 3 of a lane are
+  // operand columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+  const int steps = rank_steps(p.rank);
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(
+      p.u + ((static_cast<size_t>(tile) * p.slots + slot) * steps + k0 / 16) * kTerms * kFragment);
+  const int to_lane = 4 * (r & 7) + (k >> 2), reg = (r >> 3) + 2 * ((k >> 1) & 1);
 #pragma unroll
   for (int i = 0; i < kTerms; ++i) {
     const __nv_bfloat16 term = __float2bfloat16_rn(u);
-    out[i * rp] = term;
+    out[2 * (i * kFragment + 4 * to_lane + reg) + (k & 1)] = term;
     const float f = __bfloat162float(term);
     u = isfinite(f) ? u - f : 0.0f;  // exact
   }
@@ -135,12 +206,12 @@ struct ExpandArgs {
   const float* logits[VSL_MAX_SLICES];
   float* out[VSL_MAX_SLICES];
   const __nv_bfloat16* b[VSL_MAX_SLICES];
-  const __nv_bfloat16* u;
-  const int32_t* ids;
+  const int32_t* plan;
+  const uint32_t* u;
   float* stats;  // may be null
-  int R, V_s, n, rank, S, B;
-  int groups;       // row groups
-  int cta_groups;   // row groups per CTA (1, 2 or 4 of its warps)
+  int V_s, rank, S, B, slots;
+  int slot_ctas;  // CTAs over the slots of all tiles
+  int tiles;
   int in_place;
 };
 
@@ -150,158 +221,221 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Tile statistics of a row of the block: the row's 4 lanes (same g) hold 8
-// logits of each quarter (v[b] = ids 16 b + 4 t ..), -inf past the slice's end.
-__device__ __forceinline__ void row_stats(const float4 (&v)[8], float* rec, int t, bool write) {
+// Tile statistics of half a block (64 ids) of a row: the row's 4 lanes (same g)
+// hold 8 logits of each of its two quarters (v[b] = ids 16 b + 4 t ..), -inf
+// past the slice's end.  Every lane of the four holds the result.
+struct HalfStats {
+  float q[2], sum, mn, am;
+};
+__device__ __forceinline__ HalfStats half_stats(const float4 (&v)[4]) {
   constexpr float kLog2e = 1.4426950408889634f;
-  float q[4], mn = INFINITY, am = INFINITY;
+  HalfStats s;
+  s.mn = INFINITY;
+  s.am = INFINITY;
+  s.q[0] = s.q[1] = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = -INFINITY;
-#pragma unroll
-  for (int b = 0; b < 8; ++b) {
+  for (int b = 0; b < 4; ++b) {
     const float x[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      q[b >> 1] = fmaxf(q[b >> 1], x[j]);
-      mn = fminf(mn, isfinite(x[j]) ? x[j] : INFINITY);
-      am = fminf(am, x[j] != 0.0f ? fabsf(x[j]) : INFINITY);
+      s.q[b >> 1] = fmaxf(s.q[b >> 1], x[j]);
+      s.mn = fminf(s.mn, isfinite(x[j]) ? x[j] : INFINITY);
+      s.am = fminf(s.am, x[j] != 0.0f ? fabsf(x[j]) : INFINITY);
     }
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = fmaxf(q[i], __shfl_xor_sync(0xFFFFFFFFu, q[i], o));
-    mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
-    am = fminf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+    s.q[0] = fmaxf(s.q[0], __shfl_xor_sync(0xFFFFFFFFu, s.q[0], o));
+    s.q[1] = fmaxf(s.q[1], __shfl_xor_sync(0xFFFFFFFFu, s.q[1], o));
+    s.mn = fminf(s.mn, __shfl_xor_sync(0xFFFFFFFFu, s.mn, o));
+    s.am = fminf(s.am, __shfl_xor_sync(0xFFFFFFFFu, s.am, o));
   }
-  const float top = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3]));
+  const float top = fmaxf(s.q[0], s.q[1]);
   const float c = isfinite(top) ? top : 0.0f;
-  float sum = 0.0f;
+  s.sum = 0.0f;
 #pragma unroll
-  for (int b = 0; b < 8; ++b)
-    sum += ex2((v[b].x - c) * kLog2e) + ex2((v[b].y - c) * kLog2e) + ex2((v[b].z - c) * kLog2e) +
-           ex2((v[b].w - c) * kLog2e);
-  sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-  sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-  if (write && t == 0) {
-    reinterpret_cast<float4*>(rec)[0] = make_float4(q[0], q[1], q[2], q[3]);
-    reinterpret_cast<float4*>(rec)[1] = make_float4(sum, mn, am, 0.0f);
-  }
+  for (int b = 0; b < 4; ++b)
+    s.sum += ex2((v[b].x - c) * kLog2e) + ex2((v[b].y - c) * kLog2e) + ex2((v[b].z - c) * kLog2e) +
+             ex2((v[b].w - c) * kLog2e);
+  s.sum += __shfl_xor_sync(0xFFFFFFFFu, s.sum, 1);
+  s.sum += __shfl_xor_sync(0xFFFFFFFFu, s.sum, 2);
+  return s;
+}
+__device__ __forceinline__ void write_stats(const HalfStats& a, const HalfStats& b, float* rec) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float ta = fmaxf(a.q[0], a.q[1]), tb = fmaxf(b.q[0], b.q[1]), top = fmaxf(ta, tb);
+  const float c = isfinite(top) ? top : 0.0f;
+  // a half without a finite maximum has the sum 0, +inf or NaN whatever it is taken relative to
+  const float sum = a.sum * (isfinite(ta) ? ex2((ta - c) * kLog2e) : 1.0f) +
+                    b.sum * (isfinite(tb) ? ex2((tb - c) * kLog2e) : 1.0f);
+  reinterpret_cast<float4*>(rec)[0] = make_float4(a.q[0], a.q[1], b.q[0], b.q[1]);
+  reinterpret_cast<float4*>(rec)[1] = make_float4(sum, fminf(a.mn, b.mn), fminf(a.am, b.am), 0.0f);
 }
 
-// A warp takes 16 rows x 128 ids (one block of a slice).  The products' N index
-// is laid over the ids so that a lane's sums are 4 consecutive ids of a row:
-// column n of the i-th product of 8 is id 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.
-__global__ void __launch_bounds__(kExpandWarps * 32) adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
+// A warp takes a unit's 16 rows x 128 ids (one block of a slice), 64 ids at a
+// time.  The products' N index is laid over the ids so that a lane's sums are 4
+// consecutive ids of a row: column n of the i-th product of 8 is id
+// 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.  The units of a CTA's warps
+// follow one another, so those of one adapter share its B in L1.
+template <int STEPS>  // rank_steps, 0: any
+__global__ void __launch_bounds__(kExpandWarps * 32, 4) adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int group_ctas = (p.groups + p.cta_groups - 1) / p.cta_groups;
-  const int group = static_cast<int>(blockIdx.x % group_ctas) * p.cta_groups + warp % p.cta_groups;
-  const int block = static_cast<int>(blockIdx.x / group_ctas) * (kExpandWarps / p.cta_groups) + warp / p.cta_groups;
-  if (group >= p.groups || block >= p.S * p.B) return;
+  const int item = static_cast<int>(blockIdx.x % p.slot_ctas) * kExpandWarps + warp;
+  const int block = static_cast<int>(blockIdx.x / p.slot_ctas);
+  const int tile = item / p.slots, slot = item - tile * p.slots;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tile >= p.tiles) return;
+  const int32_t* plan = p.plan + tile * plan_ints(p.slots);
+  if (slot >= plan[0]) return;
+  const int32_t* entry = plan + 4 + slot * (kPlanUnit + 3);
+  const int adapter = entry[0];
+  if (adapter < 0 && p.in_place && p.stats == nullptr) return;  // the base logits stay as they are
   const int slice = block / p.B;
   const int j0 = (block - slice * p.B) * 128;
-  const int row0 = group * kGroup;
-  const int mine = adapter_of(p.ids, row0 + (lane & 15), p.R, p.n);
-  uint32_t left = __ballot_sync(0xFFFFFFFFu, mine >= 0) & 0xFFFFu;
-  if (p.in_place && left == 0 && p.stats == nullptr) return;  // the base logits stay as they are
-  const int r[2] = {row0 + g, row0 + g + 8};
+  const int r[2] = {entry[4 + g], entry[4 + g + 8]};
   const size_t base[2] = {static_cast<size_t>(r[0]) * p.V_s + j0 + 4 * t, static_cast<size_t>(r[1]) * p.V_s + j0 + 4 * t};
-  float4 x[2][8];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (r[i] < p.R && j0 + 16 * b + 4 * t < p.V_s)
-        x[i][b] = *reinterpret_cast<const float4*>(p.logits[slice] + base[i] + 16 * b);
-    }
-  const int rp = padded_rank(p.rank);
+  const int steps = STEPS > 0 ? STEPS : rank_steps(p.rank);
+  const uint4* u = reinterpret_cast<const uint4*>(
+      p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment) + lane;
   const uint2 zero = make_uint2(0, 0);
-  const __nv_bfloat16* u_row[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    u_row[i] = p.u + static_cast<size_t>(r[i] < p.R ? r[i] : row0) * kTerms * rp + 4 * t;
   const int n_id = 4 * (g >> 1) + (g & 1);  // the id of this lane's column, within 16 ids, of an even product
-  while (left) {
-    const int adapter = __shfl_sync(0xFFFFFFFFu, mine, __ffs(left) - 1);
-    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, mine == adapter) & 0xFFFFu;
-    left &= ~rows;
-    const bool own[2] = {((rows >> g) & 1u) != 0, ((rows >> (g + 8)) & 1u) != 0};
-    const __nv_bfloat16* b_base = p.b[slice] + (static_cast<size_t>(adapter) * p.V_s + j0) * p.rank + 4 * t;
+  HalfStats stats[2][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+  for (int half = 0; half < 2; ++half) {
+    const int jh = j0 + 64 * half;
+    float4 x[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
+          x[i][b] = *reinterpret_cast<const float4*>(p.logits[slice] + base[i] + 64 * half + 16 * b);
+      }
+    if (adapter >= 0) {
+      const __nv_bfloat16* b_base = p.b[slice] + (static_cast<size_t>(adapter) * p.V_s + jh) * p.rank + 4 * t;
       float d[8][4] = {};
-      for (int k = 0; k < rp; k += 16) {
+#pragma unroll
+      for (int k = 0; k < steps; ++k) {
         uint2 y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int j = 64 * half + 16 * (i >> 1) + 2 * (i & 1) + n_id;
-          y[i] = j0 + j < p.V_s && k + 4 * t < p.rank
-                     ? __ldg(reinterpret_cast<const uint2*>(b_base + static_cast<size_t>(j) * p.rank + k))
+          const int j = 16 * (i >> 1) + 2 * (i & 1) + n_id;
+          y[i] = jh + j < p.V_s && 16 * k + 4 * t < p.rank
+                     ? __ldg(reinterpret_cast<const uint2*>(b_base + static_cast<size_t>(j) * p.rank + 16 * k))
                      : zero;
         }
 #pragma unroll
         for (int e = 0; e < kTerms; ++e) {
-          // a row of another adapter is computed too and not kept: zeros stand in for a row that has no u
-          const uint2 u0 = own[0] ? *reinterpret_cast<const uint2*>(u_row[0] + e * rp + k) : zero;
-          const uint2 u1 = own[1] ? *reinterpret_cast<const uint2*>(u_row[1] + e * rp + k) : zero;
+          const uint4 a = u[(k * kTerms + e) * 32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mma_16816(d[i], u0.x, u1.x, u0.y, u1.y, y[i].x, y[i].y);
+          for (int i = 0; i < 8; ++i) mma_16816(d[i], a.x, a.y, a.z, a.w, y[i].x, y[i].y);
         }
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (own[i]) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float4& v = x[i][4 * half + b];
-            v.x += d[2 * b][2 * i];
-            v.y += d[2 * b][2 * i + 1];
-            v.z += d[2 * b + 1][2 * i];
-            v.w += d[2 * b + 1][2 * i + 1];
-          }
+        for (int b = 0; b < 4; ++b) {
+          x[i][b].x += d[2 * b][2 * i];
+          x[i][b].y += d[2 * b][2 * i + 1];
+          x[i][b].z += d[2 * b + 1][2 * i];
+          x[i][b].w += d[2 * b + 1][2 * i + 1];
         }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int b = 0; b < 8; ++b)
-      if (r[i] < p.R && j0 + 16 * b + 4 * t < p.V_s)
-        *reinterpret_cast<float4*>(p.out[slice] + base[i] + 16 * b) = x[i][b];
-  if (p.stats != nullptr) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      row_stats(x[i], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8, t, r[i] < p.R);
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
+          *reinterpret_cast<float4*>(p.out[slice] + base[i] + 64 * half + 16 * b) = x[i][b];
+    if (p.stats != nullptr) {
+      stats[0][half] = half_stats(x[0]);
+      stats[1][half] = half_stats(x[1]);
+    }
+  }
+  if (p.stats != nullptr && t == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (r[i] >= 0)
+        write_stats(stats[i][0], stats[i][1], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
   }
 }
 
 }  // namespace
 
-size_t adapters_workspace_bytes(int R, int rank) {
-  return (static_cast<size_t>(R) * kTerms * padded_rank(rank) * sizeof(__nv_bfloat16) + 15) / 16 * 16;
+namespace {
+
+struct AdapterSizes {
+  int tiles, slots;
+  size_t plan_bytes, u_bytes;  // each a multiple of 16
+};
+AdapterSizes adapter_sizes(int R, int n, int rank) {
+  AdapterSizes z;
+  z.tiles = (R + kTile - 1) / kTile;
+  z.slots = unit_slots(R < kTile ? R : kTile, n);
+  z.plan_bytes = static_cast<size_t>(z.tiles) * plan_ints(z.slots) * sizeof(int32_t);
+  z.u_bytes = static_cast<size_t>(z.tiles) * z.slots * rank_steps(rank) * kTerms * kFragment * sizeof(uint32_t);
+  return z;
+}
+
+template <typename Args>
+cudaError_t launch_after(void (*kernel)(Args), const Args& a, unsigned grid, cudaStream_t stream) {
+  // may start before the kernel ahead of it ends; waits for its results itself
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kExpandWarps * 32);
+  cfg.stream = stream;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+size_t adapters_workspace_bytes(int R, int n, int rank) {
+  const AdapterSizes z = adapter_sizes(R, n, rank);
+  return z.plan_bytes + z.u_bytes;
 }
 
 cudaError_t launch_adapters_add(const float* const* logits, float* const* out, const void* hidden, int R, int H, int S,
                                 int V_s, const void* a, const void* const* b, const float* scale, int n, int rank,
                                 const int32_t* ids, float* stats, void* workspace, cudaStream_t stream) {
-  const int groups = (R + kGroup - 1) / kGroup;
+  const AdapterSizes z = adapter_sizes(R, n, rank);
   ShrinkArgs sa{};
   sa.hidden = static_cast<const __nv_bfloat16*>(hidden);
   sa.a = static_cast<const __nv_bfloat16*>(a);
   sa.scale = scale;
   sa.ids = ids;
-  sa.u = static_cast<__nv_bfloat16*>(workspace);
+  sa.plan = static_cast<int32_t*>(workspace);
+  sa.u = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + z.plan_bytes);
   sa.R = R;
   sa.H = H;
   sa.n = n;
   sa.rank = rank;
-  const int distinct = R < kGroup ? R : kGroup;
-  const dim3 shrink_grid(groups, n < distinct ? n : distinct, padded_rank(rank) / 16);
-  adapters_shrink_kernel<<<shrink_grid, kShrinkWarps * 32, 0, stream>>>(sa);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  sa.slots = z.slots;
+  // a CTA takes 256 columns of H a step: the CTAs of a cluster share longer rows
+  sa.split = H >= 4 * 256 ? kMaxSplit : 1;
+  {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    cfg.gridDim = dim3(z.tiles, z.slots, rank_steps(rank) * sa.split);
+    cfg.blockDim = dim3(kShrinkWarps * 32);
+    cfg.stream = stream;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = sa.split;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, adapters_shrink_kernel, sa);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   ExpandArgs ea{};
   ea.in_place = 1;
   for (int s = 0; s < S; ++s) {
@@ -310,23 +444,23 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
     ea.b[s] = static_cast<const __nv_bfloat16*>(b[s]);
     if (logits[s] != out[s]) ea.in_place = 0;
   }
+  ea.plan = sa.plan;
   ea.u = sa.u;
-  ea.ids = ids;
   ea.stats = stats;
-  ea.R = R;
   ea.V_s = V_s;
-  ea.n = n;
   ea.rank = rank;
   ea.S = S;
   ea.B = (V_s + 127) / 128;
-  ea.groups = groups;
-  ea.cta_groups = groups >= 4 ? 4 : groups >= 2 ? 2 : 1;
-  const long long group_ctas = (groups + ea.cta_groups - 1) / ea.cta_groups;
-  const long long block_ctas = (static_cast<long long>(S) * ea.B + kExpandWarps / ea.cta_groups - 1) /
-                               (kExpandWarps / ea.cta_groups);
-  if (group_ctas * block_ctas > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  adapters_expand_kernel<<<static_cast<unsigned>(group_ctas * block_ctas), kExpandWarps * 32, 0, stream>>>(ea);
-  return cudaGetLastError();
+  ea.slots = z.slots;
+  ea.tiles = z.tiles;
+  ea.slot_ctas = static_cast<int>((static_cast<long long>(z.tiles) * z.slots + kExpandWarps - 1) / kExpandWarps);
+  const long long grid = static_cast<long long>(ea.slot_ctas) * S * ea.B;
+  if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  auto kernel = adapters_expand_kernel<0>;
+  if (rank_steps(rank) == 1) kernel = adapters_expand_kernel<1>;
+  if (rank_steps(rank) == 2) kernel = adapters_expand_kernel<2>;
+  if (rank_steps(rank) == 4) kernel = adapters_expand_kernel<4>;
+  return launch_after(kernel, ea, static_cast<unsigned>(grid), stream);
 }
 
 }  // namespace vsl

@@ -198,9 +198,9 @@ vsl_status vsl_verify_drafts(const int32_t* token_ids, const float* token_logpro
   return e == cudaSuccess ? VSL_OK : VSL_ERR_CUDA;
 }
 
-size_t vsl_adapters_workspace_bytes(int32_t R, int32_t rank) {
-  if (R <= 0 || rank <= 0) return 0;
-  return vsl::adapters_workspace_bytes(R, rank);
+size_t vsl_adapters_workspace_bytes(int32_t R, int32_t n_adapters, int32_t rank) {
+  if (R <= 0 || n_adapters <= 0 || rank <= 0 || rank > VSL_MAX_RANK) return 0;
+  return vsl::adapters_workspace_bytes(R, n_adapters, rank);
 }
 
 vsl_status vsl_adapters_add(const float* const* logits_slices, float* const* out_slices, const void* hidden_bf16,
@@ -228,7 +228,7 @@ vsl_status vsl_adapters_add(const float* const* logits_slices, float* const* out
   if (tile_stats != nullptr && !vsl::aligned32(tile_stats)) return VSL_ERR_ALIGNMENT;
   if (workspace == nullptr) return VSL_ERR_INVALID_ARG;
   if (!vsl::aligned16(workspace)) return VSL_ERR_ALIGNMENT;
-  if (workspace_bytes < vsl_adapters_workspace_bytes(R, rank)) return VSL_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < vsl_adapters_workspace_bytes(R, n_adapters, rank)) return VSL_ERR_WORKSPACE_TOO_SMALL;
   const cudaError_t e =
       vsl::launch_adapters_add(logits_slices, out_slices, hidden_bf16, R, H, S, V_s, a_bf16, b_slices_bf16, scale,
                                n_adapters, rank, adapter_ids, tile_stats, workspace, static_cast<cudaStream_t>(stream));

@@ -41,7 +41,7 @@ cudaError_t launch_verify(const int32_t* token_ids, const float* token_logprob, 
                           cudaStream_t stream);
 
 // Low-rank adapters: workspace and launch.  Arguments already validated.
-size_t adapters_workspace_bytes(int R, int rank);
+size_t adapters_workspace_bytes(int R, int n, int rank);
 cudaError_t launch_adapters_add(const float* const* logits, float* const* out, const void* hidden, int R, int H, int S,
                                 int V_s, const void* a, const void* const* b, const float* scale, int n, int rank,
                                 const int32_t* ids, float* stats, void* workspace, cudaStream_t stream);
