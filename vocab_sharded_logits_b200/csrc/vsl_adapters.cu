@@ -35,7 +35,9 @@ constexpr int kTerms = 3;         // bf16 terms of u
 constexpr int kFragment = 32 * 4; // 32-bit registers of one A operand (16 x 16 bf16) over a warp
 constexpr int kMaxSplit = 4;      // CTAs that share H
 
-__host__ __device__ constexpr int rank_steps(int rank) { return (rank + 15) / 16; }
+// Products of 16 ranks: one, or an even number (a lane then loads 8 ranks of B
+// at a time, which serve two).
+__host__ __device__ constexpr int rank_steps(int rank) { return rank <= 16 ? 1 : (rank + 31) / 32 * 2; }
 // Units a tile of `rows` rows over n adapters can have: full ones, a ragged one
 // per adapter and one of rows without an adapter.
 __host__ __device__ constexpr int unit_slots(int rows, int n) {
@@ -186,17 +188,22 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
   u = parts[0][r][k];
   for (int c = 1; c < p.split; ++c) u += parts[c][r][k];
   if (p.scale != nullptr) u *= p.scale[adapter];
-  // the second kernel's A operand: register i of lane 4 (r mod 8) + k / 4 holds the ranks of one row whose
-  // position in it, 2 * (k mod 4 / 2) .., its lanes' B take as well: ranks 4 t .. 4 t + 3 of a lane are
-  // operand columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+  // Where the second kernel's A operand has this rank.  A lane's B holds 4
+  // consecutive ranks (one step: operand columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9)
+  // or 8 (two steps, 4 each); the operand's registers are (row g, columns 2 t ..),
+  // (row g + 8, 2 t ..), (row g, 2 t + 8 ..), (row g + 8, 2 t + 8 ..).
   const int steps = rank_steps(p.rank);
+  const int rank = k0 + k, in_block = rank & 31;
+  const int of_lane = steps == 1 ? rank & 3 : in_block & 7, quad = steps == 1 ? rank >> 2 : in_block >> 3;
+  const int step = steps == 1 ? 0 : rank / 32 * 2 + (of_lane >> 2);
+  const int reg = (r >> 3) + 2 * ((of_lane >> 1) & 1);
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(
-      p.u + ((static_cast<size_t>(tile) * p.slots + slot) * steps + k0 / 16) * kTerms * kFragment);
-  const int to_lane = 4 * (r & 7) + (k >> 2), reg = (r >> 3) + 2 * ((k >> 1) & 1);
+                           p.u + ((static_cast<size_t>(tile) * p.slots + slot) * steps + step) * kTerms * kFragment) +
+                       2 * (4 * (4 * (r & 7) + quad) + reg) + (rank & 1);
 #pragma unroll
   for (int i = 0; i < kTerms; ++i) {
     const __nv_bfloat16 term = __float2bfloat16_rn(u);
-    out[2 * (i * kFragment + 4 * to_lane + reg) + (k & 1)] = term;
+    out[2 * i * kFragment] = term;
     const float f = __bfloat162float(term);
     u = isfinite(f) ? u - f : 0.0f;  // exact
   }
@@ -210,7 +217,8 @@ struct ExpandArgs {
   const uint32_t* u;
   float* stats;  // may be null
   int V_s, rank, S, B, slots;
-  int slot_ctas;  // CTAs over the slots of all tiles
+  int slot_ctas;   // CTAs over the slots of all tiles
+  int warp_blocks; // blocks of 128 ids a warp takes
   int tiles;
   int in_place;
 };
@@ -272,93 +280,154 @@ __device__ __forceinline__ void write_stats(const HalfStats& a, const HalfStats&
   reinterpret_cast<float4*>(rec)[1] = make_float4(sum, fminf(a.mn, b.mn), fminf(a.am, b.am), 0.0f);
 }
 
-// A warp takes a unit's 16 rows x 128 ids (one block of a slice), 64 ids at a
-// time.  The products' N index is laid over the ids so that a lane's sums are 4
-// consecutive ids of a row: column n of the i-th product of 8 is id
-// 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.  The units of a CTA's warps
-// follow one another, so those of one adapter share its B in L1.
-template <int STEPS>  // rank_steps, 0: any
-__global__ void __launch_bounds__(kExpandWarps * 32, 4) adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
+// A lane's part of B for 64 ids: 4 ranks of an id's row to a load, or 8.
+template <int STEPS>
+struct BLoad {
+  uint4 v[8];
+};
+template <>
+struct BLoad<1> {
+  uint2 v[8];
+};
+
+__device__ __forceinline__ void load_b(uint2& v, const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+__device__ __forceinline__ void load_b(uint4& v, const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+
+// Operand i of u: from registers, shared memory or global memory.
+template <int STEPS, typename Reg, typename Shared>
+__device__ __forceinline__ uint4 operand(const Reg& reg, const Shared& shared, const uint4* u, int warp, int lane, int i) {
+  if constexpr (STEPS == 1 || STEPS == 2) return reg[i];
+  if constexpr (STEPS == 4) return shared[warp][i][lane];
+  return u[i * 32];
+}
+template <int STEPS, typename Reg, typename Shared>
+__device__ __forceinline__ void second_step(float (&d)[8][4], const BLoad<STEPS>& y, const Reg& reg,
+                                            const Shared& shared, const uint4* u, int warp, int lane, int k) {
+  if constexpr (STEPS != 1) {
+#pragma unroll
+    for (int e = 0; e < kTerms; ++e) {
+      const uint4 a = operand<STEPS>(reg, shared, u, warp, lane, (k + 1) * kTerms + e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma_16816(d[i], a.x, a.y, a.z, a.w, y.v[i].z, y.v[i].w);
+    }
+  }
+}
+
+// A warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice),
+// 64 ids at a time.  The products' N index is laid over the ids so that a
+// lane's sums are 4 consecutive ids of a row: column n of the i-th product of 8
+// is id 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.  The units of a CTA's
+// warps follow one another, so those of one adapter share its B in L1.
+template <int STEPS>  // rank_steps, 0: any even number
+__global__ void __launch_bounds__(kExpandWarps * 32, STEPS == 1 || STEPS == 2 ? 4 : 3) adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
+  // u stays in registers for one or two steps, in shared memory for four
+  constexpr bool kInRegs = STEPS == 1 || STEPS == 2;
+  __shared__ uint4 u_shared[STEPS == 4 ? kExpandWarps : 1][STEPS == 4 ? 4 * kTerms : 1][STEPS == 4 ? 32 : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int item = static_cast<int>(blockIdx.x % p.slot_ctas) * kExpandWarps + warp;
-  const int block = static_cast<int>(blockIdx.x / p.slot_ctas);
+  const int block0 = static_cast<int>(blockIdx.x / p.slot_ctas) * p.warp_blocks;
   const int tile = item / p.slots, slot = item - tile * p.slots;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tile >= p.tiles) return;
   const int32_t* plan = p.plan + tile * plan_ints(p.slots);
-  if (slot >= plan[0]) return;
   const int32_t* entry = plan + 4 + slot * (kPlanUnit + 3);
+  if (slot >= plan[0]) return;
   const int adapter = entry[0];
   if (adapter < 0 && p.in_place && p.stats == nullptr) return;  // the base logits stay as they are
-  const int slice = block / p.B;
-  const int j0 = (block - slice * p.B) * 128;
   const int r[2] = {entry[4 + g], entry[4 + g + 8]};
-  const size_t base[2] = {static_cast<size_t>(r[0]) * p.V_s + j0 + 4 * t, static_cast<size_t>(r[1]) * p.V_s + j0 + 4 * t};
   const int steps = STEPS > 0 ? STEPS : rank_steps(p.rank);
   const uint4* u = reinterpret_cast<const uint4*>(
       p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment) + lane;
-  const uint2 zero = make_uint2(0, 0);
+  uint4 u_reg[kInRegs ? STEPS * kTerms : 1];
+  if (adapter >= 0) {
+    if (kInRegs) {
+#pragma unroll
+      for (int i = 0; i < STEPS * kTerms; ++i) u_reg[i] = u[i * 32];
+    }
+    if (STEPS == 4) {
+#pragma unroll
+      for (int i = 0; i < 4 * kTerms; ++i) u_shared[warp][i][lane] = u[i * 32];  // a lane reads its own back
+    }
+  }
   const int n_id = 4 * (g >> 1) + (g & 1);  // the id of this lane's column, within 16 ids, of an even product
-  HalfStats stats[2][2];
+  constexpr int kLaneRanks = STEPS == 1 ? 4 : 8;  // of one load
+  const int last_block = min(block0 + p.warp_blocks, p.S * p.B);
+  int slice = block0 / p.B, in_slice = block0 - slice * p.B;
+#pragma unroll 1
+  for (int block = block0; block < last_block; ++block, ++in_slice) {
+    if (in_slice == p.B) {
+      in_slice = 0;
+      ++slice;
+    }
+    const int j0 = in_slice * 128;
+    const size_t base[2] = {static_cast<size_t>(r[0]) * p.V_s + j0 + 4 * t,
+                            static_cast<size_t>(r[1]) * p.V_s + j0 + 4 * t};
+    const float* src = p.logits[slice];
+    float* dst = p.out[slice];
+    HalfStats stats[2][2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int jh = j0 + 64 * half;
-    float4 x[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
-          x[i][b] = *reinterpret_cast<const float4*>(p.logits[slice] + base[i] + 64 * half + 16 * b);
-      }
-    if (adapter >= 0) {
-      const __nv_bfloat16* b_base = p.b[slice] + (static_cast<size_t>(adapter) * p.V_s + jh) * p.rank + 4 * t;
-      float d[8][4] = {};
-#pragma unroll
-      for (int k = 0; k < steps; ++k) {
-        uint2 y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = 16 * (i >> 1) + 2 * (i & 1) + n_id;
-          y[i] = jh + j < p.V_s && 16 * k + 4 * t < p.rank
-                     ? __ldg(reinterpret_cast<const uint2*>(b_base + static_cast<size_t>(j) * p.rank + 16 * k))
-                     : zero;
-        }
-#pragma unroll
-        for (int e = 0; e < kTerms; ++e) {
-          const uint4 a = u[(k * kTerms + e) * 32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) mma_16816(d[i], a.x, a.y, a.z, a.w, y[i].x, y[i].y);
-        }
-      }
+    for (int half = 0; half < 2; ++half) {
+      const int jh = j0 + 64 * half;
+      float4 x[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          x[i][b].x += d[2 * b][2 * i];
-          x[i][b].y += d[2 * b][2 * i + 1];
-          x[i][b].z += d[2 * b + 1][2 * i];
-          x[i][b].w += d[2 * b + 1][2 * i + 1];
+          x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
+            x[i][b] = *reinterpret_cast<const float4*>(src + base[i] + 64 * half + 16 * b);
         }
+      if (adapter >= 0) {
+        // ids past the slice's end read its last one's row instead (their sums are not kept)
+        const int most = p.V_s - 1 - jh;
+        const __nv_bfloat16* b_base = p.b[slice] + (static_cast<size_t>(adapter) * p.V_s + jh) * p.rank + kLaneRanks * t;
+        float d[8][4] = {};
+#pragma unroll
+        for (int k = 0; k < steps; k += STEPS == 1 ? 1 : 2) {
+          BLoad<STEPS> y;
+          const bool ranks_in = 16 * k + kLaneRanks * t < p.rank;  // past the rank: zeros
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = min(16 * (i >> 1) + 2 * (i & 1) + n_id, most);
+            y.v[i] = {};
+            if (ranks_in) load_b(y.v[i], b_base + j * p.rank + 16 * k);
+          }
+#pragma unroll
+          for (int e = 0; e < kTerms; ++e) {
+            const uint4 a = operand<STEPS>(u_reg, u_shared, u, warp, lane, k * kTerms + e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mma_16816(d[i], a.x, a.y, a.z, a.w, y.v[i].x, y.v[i].y);
+          }
+          second_step<STEPS>(d, y, u_reg, u_shared, u, warp, lane, k);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            x[i][b].x += d[2 * b][2 * i];
+            x[i][b].y += d[2 * b][2 * i + 1];
+            x[i][b].z += d[2 * b + 1][2 * i];
+            x[i][b].w += d[2 * b + 1][2 * i + 1];
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
+            *reinterpret_cast<float4*>(dst + base[i] + 64 * half + 16 * b) = x[i][b];
+      if (p.stats != nullptr) {
+        stats[0][half] = half_stats(x[0]);
+        stats[1][half] = half_stats(x[1]);
+      }
     }
+    if (p.stats != nullptr && t == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
-          *reinterpret_cast<float4*>(p.out[slice] + base[i] + 64 * half + 16 * b) = x[i][b];
-    if (p.stats != nullptr) {
-      stats[0][half] = half_stats(x[0]);
-      stats[1][half] = half_stats(x[1]);
+      for (int i = 0; i < 2; ++i)
+        if (r[i] >= 0)
+          write_stats(stats[i][0], stats[i][1], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
     }
-  }
-  if (p.stats != nullptr && t == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (r[i] >= 0)
-        write_stats(stats[i][0], stats[i][1], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
   }
 }
 
@@ -454,7 +523,12 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   ea.slots = z.slots;
   ea.tiles = z.tiles;
   ea.slot_ctas = static_cast<int>((static_cast<long long>(z.tiles) * z.slots + kExpandWarps - 1) / kExpandWarps);
-  const long long grid = static_cast<long long>(ea.slot_ctas) * S * ea.B;
+  // a warp keeps its unit's u over several blocks, while there are warps enough to fill the SMs some times over
+  ea.warp_blocks = 1;
+  while (ea.warp_blocks < 8 && static_cast<long long>(ea.slot_ctas) * S * ea.B / ea.warp_blocks > 8 * 148 * 4)
+    ea.warp_blocks *= 2;
+  const long long grid =
+      static_cast<long long>(ea.slot_ctas) * ((static_cast<long long>(S) * ea.B + ea.warp_blocks - 1) / ea.warp_blocks);
   if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   auto kernel = adapters_expand_kernel<0>;
   if (rank_steps(rank) == 1) kernel = adapters_expand_kernel<1>;
