@@ -34,6 +34,7 @@ constexpr int kExpandWarps = 4;
 constexpr int kTerms = 3;         // bf16 terms of u
 constexpr int kFragment = 32 * 4; // 32-bit registers of one A operand (16 x 16 bf16) over a warp
 constexpr int kMaxSplit = 4;      // CTAs that share H
+constexpr int kFewRows = 2;       // a unit of so few rows is done with float32 multiply-adds
 
 // Products of 16 ranks: one, or an even number (a lane then loads 8 ranks of B
 // at a time, which serve two).
@@ -45,8 +46,8 @@ __host__ __device__ constexpr int unit_slots(int rows, int n) {
   return rows / kUnitRows + distinct < rows ? rows / kUnitRows + distinct : rows;
 }
 
-// The plan of a tile: its units' number, then a unit's adapter (-1: none) and
-// rows (-1: none) each.
+// The plan of a tile: its units' number, then of each unit the adapter (-1:
+// none), the number of rows and (from the fifth word on) the rows, -1 past them.
 constexpr int kPlanUnit = 1 + kUnitRows;
 __host__ __device__ constexpr size_t plan_ints(int slots) { return 4 + static_cast<size_t>(slots) * (kPlanUnit + 3); }
 __device__ __forceinline__ int32_t* plan_unit(int32_t* plan, int slot) { return plan + 4 + slot * (kPlanUnit + 3); }
@@ -68,7 +69,8 @@ struct ShrinkArgs {
   const float* scale;  // may be null: 1
   const int32_t* ids;
   int32_t* plan;       // [tiles][plan_ints(slots)]
-  uint32_t* u;         // [tiles][slots][steps][kTerms][kFragment]: as the second kernel's lanes hold it
+  uint32_t* u;         // [tiles][slots][steps][kTerms][kFragment]: as the second kernel's lanes hold it, or
+                       // in a unit of few rows [row][rank] float32
   int R, H, n, rank, slots, split;
 };
 
@@ -134,6 +136,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
     int32_t* entry = plan_unit(plan, slot);
     if (tid < kUnitRows) entry[4 + tid] = tid < count ? row0 + order[first + tid] : -1;
     if (tid == kUnitRows) entry[0] = adapter;
+    if (tid == kUnitRows + 1) entry[1] = count;
   }
   if (adapter < 0) return;
 
@@ -193,6 +196,11 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
   // or 8 (two steps, 4 each); the operand's registers are (row g, columns 2 t ..),
   // (row g + 8, 2 t ..), (row g, 2 t + 8 ..), (row g + 8, 2 t + 8 ..).
   const int steps = rank_steps(p.rank);
+  if (count <= kFewRows) {  // kept as it is, [row][padded rank]
+    float* rows_u = reinterpret_cast<float*>(p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment);
+    if (r < count) rows_u[r * steps * 16 + k0 + k] = u;
+    return;
+  }
   const int rank = k0 + k, in_block = rank & 31;
   const int of_lane = steps == 1 ? rank & 3 : in_block & 7, quad = steps == 1 ? rank >> 2 : in_block >> 3;
   const int step = steps == 1 ? 0 : rank / 32 * 2 + (of_lane >> 2);
@@ -313,13 +321,148 @@ __device__ __forceinline__ void second_step(float (&d)[8][4], const BLoad<STEPS>
   }
 }
 
+// Tile statistics of a row of a block whose quarter m is spread over the warp
+// as v[m] (-inf past the slice's end).
+__device__ __forceinline__ void warp_stats(const float (&v)[4], float* rec, int lane) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  float q[4], mn = INFINITY, am = INFINITY;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    q[m] = v[m];
+    mn = fminf(mn, isfinite(v[m]) ? v[m] : INFINITY);
+    am = fminf(am, v[m] != 0.0f ? fabsf(v[m]) : INFINITY);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) q[m] = fmaxf(q[m], __shfl_xor_sync(0xFFFFFFFFu, q[m], o));
+    mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
+    am = fminf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+  }
+  const float top = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3]));
+  const float c = isfinite(top) ? top : 0.0f;
+  float sum = 0.0f;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) sum += ex2((v[m] - c) * kLog2e);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) {
+    reinterpret_cast<float4*>(rec)[0] = make_float4(q[0], q[1], q[2], q[3]);
+    reinterpret_cast<float4*>(rec)[1] = make_float4(sum, mn, am, 0.0f);
+  }
+}
+
+__device__ __forceinline__ float dot8(const uint4& b, const float (&u)[8], float sum) {
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum = __fmaf_rn(__uint_as_float(w[i] << 16), u[2 * i], sum);
+    sum = __fmaf_rn(__uint_as_float(w[i] & 0xFFFF0000u), u[2 * i + 1], sum);
+  }
+  return sum;
+}
+
+// Up to ROWS rows of a unit of at most kFewRows over blocks of 128 ids: 15 of 16 rows of a
+// tensor-core product would be empty, and what counts is that B, which no other
+// row shares, streams in.  LANES lanes hold an id's row of B, 8 ranks each: a
+// quarter (32 ids) is LANES loads of 512 contiguous bytes.  The lanes' sums are
+// added and dealt out in one butterfly, after which every lane holds one id of
+// the quarter: LANES' lane `sub` of the ids' group `at` id (32 / LANES) sub + at.
+template <int LANES, int ROWS>
+__device__ __forceinline__ void few_rows(const ExpandArgs& p, int adapter, const int32_t* rows, int count, const float* u_rows,
+                                         int padded, int block0, int last_block, int lane) {
+  constexpr int kPer = 32 / LANES;              // ids of one load
+  constexpr int kLoads = LANES < 8 ? LANES : 8; // loads of a quarter in flight
+  constexpr int kQuarters = LANES < 8 ? (LANES < 2 ? 4 : 8 / LANES) : 1;  // quarters in flight
+  const int sub = lane % LANES, at = lane / LANES;
+  const bool ranks_in = 8 * sub < p.rank;
+  float u[ROWS][8];
+  int row[ROWS];
+#pragma unroll
+  for (int c = 0; c < ROWS; ++c) {
+    row[c] = rows[c < count ? c : 0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[c][i] = c < count && ranks_in ? u_rows[c * padded + 8 * sub + i] : 0.0f;
+  }
+  int slice = block0 / p.B, in_slice = block0 - slice * p.B;
+#pragma unroll 1
+  for (int block = block0; block < last_block; ++block, ++in_slice) {
+    if (in_slice == p.B) {
+      in_slice = 0;
+      ++slice;
+    }
+    const int j0 = in_slice * 128, most = p.V_s - 1 - j0;
+    const __nv_bfloat16* b = p.b[slice] + (static_cast<size_t>(adapter) * p.V_s + j0) * p.rank + 8 * sub;
+    const int mine = kPer * sub + at;  // this lane's id of a quarter
+    float v[ROWS][4];
+#pragma unroll
+    for (int c = 0; c < ROWS; ++c)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        v[c][m] = -INFINITY;
+        if (c < count && 32 * m + mine <= most)
+          v[c][m] = p.logits[slice][static_cast<size_t>(row[c]) * p.V_s + j0 + 32 * m + mine];
+      }
+#pragma unroll
+    for (int m0 = 0; m0 < 4; m0 += kQuarters) {
+      float part[ROWS][kQuarters][LANES];
+#pragma unroll
+      for (int i0 = 0; i0 < LANES; i0 += kLoads) {
+        uint4 y[kQuarters][kLoads];
+#pragma unroll
+        for (int q = 0; q < kQuarters; ++q)
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            y[q][i] = make_uint4(0, 0, 0, 0);
+            // ids past the slice's end read its last one's row instead (their sums are not kept)
+            if (ranks_in) load_b(y[q][i], b + min(32 * (m0 + q) + kPer * (i0 + i) + at, most) * p.rank);
+          }
+#pragma unroll
+        for (int q = 0; q < kQuarters; ++q)
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) {
+            part[0][q][i0 + i] = dot8(y[q][i], u[0], 0.0f);
+#pragma unroll
+            for (int c = 1; c < ROWS; ++c) part[c][q][i0 + i] = count > c ? dot8(y[q][i], u[c], 0.0f) : 0.0f;
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < ROWS; ++c)
+        if (c < count) {  // the warp's: a butterfly takes all its lanes
+#pragma unroll
+          for (int q = 0; q < kQuarters; ++q) {
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+              for (int i = 0; i < o; ++i) {
+                const float keep = (sub & o) ? part[c][q][i + o] : part[c][q][i];
+                const float give = (sub & o) ? part[c][q][i] : part[c][q][i + o];
+                part[c][q][i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+              }
+            v[c][m0 + q] += part[c][q][0];
+          }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < ROWS; ++c)
+      if (c < count) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (32 * m + mine <= most)
+            p.out[slice][static_cast<size_t>(row[c]) * p.V_s + j0 + 32 * m + mine] = v[c][m];
+        if (p.stats != nullptr) warp_stats(v[c], p.stats + (static_cast<size_t>(row[c]) * p.S * p.B + block) * 8, lane);
+      }
+  }
+}
+
 // A warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice),
 // 64 ids at a time.  The products' N index is laid over the ids so that a
 // lane's sums are 4 consecutive ids of a row: column n of the i-th product of 8
 // is id 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.  The units of a CTA's
 // warps follow one another, so those of one adapter share its B in L1.
-template <int STEPS>  // rank_steps, 0: any even number
-__global__ void __launch_bounds__(kExpandWarps * 32, STEPS == 1 || STEPS == 2 ? 4 : 3) adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
+template <int STEPS, int LANES>  // rank_steps (0: any even number), lanes of 8 ranks in few_rows
+__global__ void __launch_bounds__(kExpandWarps * 32, STEPS == 1 || STEPS == 2 ? 4 : 3)
+    adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
   // u stays in registers for one or two steps, in shared memory for four
   constexpr bool kInRegs = STEPS == 1 || STEPS == 2;
   __shared__ uint4 u_shared[STEPS == 4 ? kExpandWarps : 1][STEPS == 4 ? 4 * kTerms : 1][STEPS == 4 ? 32 : 1];
@@ -335,8 +478,18 @@ __global__ void __launch_bounds__(kExpandWarps * 32, STEPS == 1 || STEPS == 2 ? 
   if (slot >= plan[0]) return;
   const int adapter = entry[0];
   if (adapter < 0 && p.in_place && p.stats == nullptr) return;  // the base logits stay as they are
-  const int r[2] = {entry[4 + g], entry[4 + g + 8]};
+  const int last_block = min(block0 + p.warp_blocks, p.S * p.B);
   const int steps = STEPS > 0 ? STEPS : rank_steps(p.rank);
+  if (adapter >= 0 && entry[1] <= kFewRows) {  // the whole warp's
+    const float* u_rows =
+        reinterpret_cast<const float*>(p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment);
+    constexpr int kAtOnce = LANES < 16 ? kFewRows : 1;  // as many as the registers hold
+    for (int c = 0; c < entry[1]; c += kAtOnce)
+      few_rows<LANES, kAtOnce>(p, adapter, entry + 4 + c, min(entry[1] - c, kAtOnce), u_rows + c * steps * 16, steps * 16,
+                               block0, last_block, lane);
+    return;
+  }
+  const int r[2] = {entry[4 + g], entry[4 + g + 8]};
   const uint4* u = reinterpret_cast<const uint4*>(
       p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment) + lane;
   uint4 u_reg[kInRegs ? STEPS * kTerms : 1];
@@ -352,7 +505,6 @@ __global__ void __launch_bounds__(kExpandWarps * 32, STEPS == 1 || STEPS == 2 ? 
   }
   const int n_id = 4 * (g >> 1) + (g & 1);  // the id of this lane's column, within 16 ids, of an even product
   constexpr int kLaneRanks = STEPS == 1 ? 4 : 8;  // of one load
-  const int last_block = min(block0 + p.warp_blocks, p.S * p.B);
   int slice = block0 / p.B, in_slice = block0 - slice * p.B;
 #pragma unroll 1
   for (int block = block0; block < last_block; ++block, ++in_slice) {
@@ -530,10 +682,12 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   const long long grid =
       static_cast<long long>(ea.slot_ctas) * ((static_cast<long long>(S) * ea.B + ea.warp_blocks - 1) / ea.warp_blocks);
   if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  auto kernel = adapters_expand_kernel<0>;
-  if (rank_steps(rank) == 1) kernel = adapters_expand_kernel<1>;
-  if (rank_steps(rank) == 2) kernel = adapters_expand_kernel<2>;
-  if (rank_steps(rank) == 4) kernel = adapters_expand_kernel<4>;
+  auto kernel = rank <= 8     ? adapters_expand_kernel<1, 1>
+                : rank <= 16  ? adapters_expand_kernel<1, 2>
+                : rank <= 32  ? adapters_expand_kernel<2, 4>
+                : rank <= 64  ? adapters_expand_kernel<4, 8>
+                : rank <= 128 ? adapters_expand_kernel<0, 16>
+                              : adapters_expand_kernel<0, 32>;
   return launch_after(kernel, ea, static_cast<unsigned>(grid), stream);
 }
 
