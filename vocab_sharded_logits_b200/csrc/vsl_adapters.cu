@@ -74,21 +74,23 @@ struct ShrinkArgs {
   int R, H, n, rank, slots, split;
 };
 
-// CTA (tile, unit, 16 ranks x a part of H): the warps split the part, the CTAs
-// of a cluster share H.
+// CTA (tile, unit, up to 16 GROUPS ranks x a part of H): the warps split the
+// part, the CTAs of a cluster share H.
+template <int GROUPS>
 __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(const __grid_constant__ ShrinkArgs p) {
   __shared__ int key[kTile];
   __shared__ int order[kTile];        // sorted position -> row of the tile
   __shared__ int within[kTile];       // sorted position -> rows of its adapter before it
   __shared__ int starts[kTile + 1];   // unit -> its first sorted position
   __shared__ int warp_units[kShrinkWarps];
-  __shared__ float part[kShrinkWarps][kUnitRows][16];
-  __shared__ float parts[kMaxSplit][kUnitRows][16];
+  constexpr int kRanks = 16 * GROUPS;
+  __shared__ float part[kShrinkWarps / 2][kUnitRows][kRanks];
+  __shared__ float parts[kMaxSplit][kUnitRows][kRanks];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const int slot = static_cast<int>(blockIdx.y), tile = static_cast<int>(blockIdx.x);
   const int split_rank = static_cast<int>(cluster_ctarank());
-  const int k0 = static_cast<int>(blockIdx.z) / p.split * 16;
+  const int k0 = static_cast<int>(blockIdx.z) / p.split * kRanks;
   const int row0 = tile * kTile, rows = min(kTile, p.R - row0);
 
   // ---- sort: rows by (adapter, row), those without an adapter last
@@ -140,80 +142,90 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
   }
   if (adapter < 0) return;
 
-  // ---- u of the unit: 16 rows x 16 ranks
+  // ---- u of the unit: 16 rows x kRanks ranks
   const int g = lane >> 2, t = lane & 3;
   const bool row_ok[2] = {g < count, g + 8 < count};
-  const bool rank_ok[2] = {k0 + g < p.rank, k0 + 8 + g < p.rank};
   const __nv_bfloat16* h_row[2];
-  const __nv_bfloat16* a_row[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 2; ++i)
     h_row[i] = p.hidden + static_cast<size_t>(row0 + order[first + (row_ok[i] ? g + 8 * i : 0)]) * p.H;
-    a_row[i] = p.a + (static_cast<size_t>(adapter) * p.rank + (rank_ok[i] ? k0 + 8 * i + g : 0)) * p.H;
-  }
-  float d[2][4] = {};
+  const __nv_bfloat16* a_row = p.a + (static_cast<size_t>(adapter) * p.rank + k0 + g) * p.H;
+  float d[2 * GROUPS][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // 32 columns of H a step: a lane's 8 consecutive ones serve two products
   // (the order of the summed index is free, the same on both sides).  The
   // loop's bound is the warp's, not the lane's: every lane takes part in a
   // product, with zeros past the end of H.
-#pragma unroll 4
+#pragma unroll (GROUPS > 2 ? 2 : 4)
   for (int h0 = (split_rank * kShrinkWarps + warp) * 32; h0 < p.H; h0 += p.split * kShrinkWarps * 32) {
     const int h = h0 + 8 * t;
     const bool in = h < p.H;
-    uint4 x[2], y[2];
+    uint4 x[2], y[2 * GROUPS];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      x[i] = in && row_ok[i] ? __ldg(reinterpret_cast<const uint4*>(h_row[i] + h)) : zero;
-      y[i] = in && rank_ok[i] ? __ldg(reinterpret_cast<const uint4*>(a_row[i] + h)) : zero;
-    }
+    for (int i = 0; i < 2; ++i) x[i] = in && row_ok[i] ? __ldg(reinterpret_cast<const uint4*>(h_row[i] + h)) : zero;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * GROUPS; ++i)
+      y[i] = in && k0 + 8 * i + g < p.rank
+                 ? __ldg(reinterpret_cast<const uint4*>(a_row + static_cast<size_t>(8 * i) * p.H + h))
+                 : zero;
+#pragma unroll
+    for (int i = 0; i < 2 * GROUPS; ++i) {
       mma_16816(d[i], x[0].x, x[1].x, x[0].y, x[1].y, y[i].x, y[i].y);
       mma_16816(d[i], x[0].z, x[1].z, x[0].w, x[1].w, y[i].z, y[i].w);
     }
   }
+  // the warps' sums: the upper four's first, then the lower four add theirs
+  float* mine_part = &part[warp % (kShrinkWarps / 2)][0][0];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    part[warp][g][8 * i + 2 * t] = d[i][0];
-    part[warp][g][8 * i + 2 * t + 1] = d[i][1];
-    part[warp][g + 8][8 * i + 2 * t] = d[i][2];
-    part[warp][g + 8][8 * i + 2 * t + 1] = d[i][3];
+  for (int round = 0; round < 2; ++round) {
+    if (warp / (kShrinkWarps / 2) == 1 - round) {
+#pragma unroll
+      for (int i = 0; i < 2 * GROUPS; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float& to = mine_part[(g + 8 * (q >> 1)) * kRanks + 8 * i + 2 * t + (q & 1)];
+          to = round == 0 ? d[i][q] : to + d[i][q];
+        }
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int r = tid >> 4, k = tid & 15;
-  float u = 0.0f;
+  for (int e = tid; e < kUnitRows * kRanks; e += kShrinkWarps * 32) {
+    float u = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kShrinkWarps; ++w) u += part[w][r][k];
-  *cluster_ptr(&parts[split_rank][r][k], 0) = u;
+    for (int w = 0; w < kShrinkWarps / 2; ++w) u += (&part[w][0][0])[e];
+    *cluster_ptr(&parts[split_rank][0][0] + e, 0) = u;
+  }
   cluster_sync();  // no access to another CTA's memory follows
   if (split_rank != 0) return;
-  u = parts[0][r][k];
-  for (int c = 1; c < p.split; ++c) u += parts[c][r][k];
-  if (p.scale != nullptr) u *= p.scale[adapter];
-  // Where the second kernel's A operand has this rank.  A lane's B holds 4
-  // consecutive ranks (one step: operand columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9)
-  // or 8 (two steps, 4 each); the operand's registers are (row g, columns 2 t ..),
-  // (row g + 8, 2 t ..), (row g, 2 t + 8 ..), (row g + 8, 2 t + 8 ..).
   const int steps = rank_steps(p.rank);
-  if (count <= kFewRows) {  // kept as it is, [row][padded rank]
-    float* rows_u = reinterpret_cast<float*>(p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment);
-    if (r < count) rows_u[r * steps * 16 + k0 + k] = u;
-    return;
-  }
-  const int rank = k0 + k, in_block = rank & 31;
-  const int of_lane = steps == 1 ? rank & 3 : in_block & 7, quad = steps == 1 ? rank >> 2 : in_block >> 3;
-  const int step = steps == 1 ? 0 : rank / 32 * 2 + (of_lane >> 2);
-  const int reg = (r >> 3) + 2 * ((of_lane >> 1) & 1);
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(
-                           p.u + ((static_cast<size_t>(tile) * p.slots + slot) * steps + step) * kTerms * kFragment) +
-                       2 * (4 * (4 * (r & 7) + quad) + reg) + (rank & 1);
+  uint32_t* unit_u = p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment;
+  for (int e = tid; e < kUnitRows * kRanks; e += kShrinkWarps * 32) {
+    const int r = e / kRanks, rank = k0 + e % kRanks;
+    if (rank >= 16 * steps) continue;
+    float u = (&parts[0][0][0])[e];
+    for (int c = 1; c < p.split; ++c) u += (&parts[c][0][0])[e];
+    if (p.scale != nullptr) u *= p.scale[adapter];
+    if (count <= kFewRows) {  // kept as it is, [row][padded rank]
+      if (r < count) reinterpret_cast<float*>(unit_u)[r * steps * 16 + rank] = u;
+      continue;
+    }
+    // Where the second kernel's A operand has this rank.  A lane's B holds 4
+    // consecutive ranks (one step: operand columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9)
+    // or 8 (two steps, 4 each); the operand's registers are (row g, columns 2 t ..),
+    // (row g + 8, 2 t ..), (row g, 2 t + 8 ..), (row g + 8, 2 t + 8 ..).
+    const int in_block = rank & 31;
+    const int of_lane = steps == 1 ? rank & 3 : in_block & 7, quad = steps == 1 ? rank >> 2 : in_block >> 3;
+    const int step = steps == 1 ? 0 : rank / 32 * 2 + (of_lane >> 2);
+    const int reg = (r >> 3) + 2 * ((of_lane >> 1) & 1);
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(unit_u + step * kTerms * kFragment) +
+                         2 * (4 * (4 * (r & 7) + quad) + reg) + (rank & 1);
 #pragma unroll
-  for (int i = 0; i < kTerms; ++i) {
-    const __nv_bfloat16 term = __float2bfloat16_rn(u);
-    out[2 * i * kFragment] = term;
-    const float f = __bfloat162float(term);
-    u = isfinite(f) ? u - f : 0.0f;  // exact
+    for (int i = 0; i < kTerms; ++i) {
+      const __nv_bfloat16 term = __float2bfloat16_rn(u);
+      out[2 * i * kFragment] = term;
+      const float v = __bfloat162float(term);
+      u = isfinite(v) ? u - v : 0.0f;  // exact
+    }
   }
 }
 
@@ -639,12 +651,15 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   sa.n = n;
   sa.rank = rank;
   sa.slots = z.slots;
-  // a CTA takes 256 columns of H a step: the CTAs of a cluster share longer rows
-  sa.split = H >= 4 * 256 ? kMaxSplit : 1;
+  // up to 64 ranks to a CTA; the CTAs of a cluster share longer rows of H while
+  // the units are few
+  const int steps = rank_steps(rank);
+  const int groups = steps < 4 ? steps : 4, ctas = z.tiles * z.slots * ((steps + groups - 1) / groups);
+  sa.split = H < 4 * 256 || ctas > 296 ? 1 : ctas > 148 ? 2 : kMaxSplit;
   {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
-    cfg.gridDim = dim3(z.tiles, z.slots, rank_steps(rank) * sa.split);
+    cfg.gridDim = dim3(z.tiles, z.slots, (steps + groups - 1) / groups * sa.split);
     cfg.blockDim = dim3(kShrinkWarps * 32);
     cfg.stream = stream;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -653,7 +668,10 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
     attr.val.clusterDim.z = sa.split;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, adapters_shrink_kernel, sa);
+    auto kernel = groups == 1   ? adapters_shrink_kernel<1>
+                  : groups == 2 ? adapters_shrink_kernel<2>
+                                : adapters_shrink_kernel<4>;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, sa);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
