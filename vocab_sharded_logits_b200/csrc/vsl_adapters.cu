@@ -19,6 +19,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
+#include <type_traits>
 
 #include "vsl_internal.h"
 #include "vsl_ptx.cuh"
@@ -300,38 +302,7 @@ __device__ __forceinline__ void write_stats(const HalfStats& a, const HalfStats&
   reinterpret_cast<float4*>(rec)[1] = make_float4(sum, fminf(a.mn, b.mn), fminf(a.am, b.am), 0.0f);
 }
 
-// A lane's part of B for 64 ids: 4 ranks of an id's row to a load, or 8.
-template <int STEPS>
-struct BLoad {
-  uint4 v[8];
-};
-template <>
-struct BLoad<1> {
-  uint2 v[8];
-};
-
-__device__ __forceinline__ void load_b(uint2& v, const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
 __device__ __forceinline__ void load_b(uint4& v, const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-
-// Operand i of u: from registers, shared memory or global memory.
-template <int STEPS, typename Reg, typename Shared>
-__device__ __forceinline__ uint4 operand(const Reg& reg, const Shared& shared, const uint4* u, int warp, int lane, int i) {
-  if constexpr (STEPS == 1 || STEPS == 2) return reg[i];
-  if constexpr (STEPS == 4) return shared[warp][i][lane];
-  return u[i * 32];
-}
-template <int STEPS, typename Reg, typename Shared>
-__device__ __forceinline__ void second_step(float (&d)[8][4], const BLoad<STEPS>& y, const Reg& reg,
-                                            const Shared& shared, const uint4* u, int warp, int lane, int k) {
-  if constexpr (STEPS != 1) {
-#pragma unroll
-    for (int e = 0; e < kTerms; ++e) {
-      const uint4 a = operand<STEPS>(reg, shared, u, warp, lane, (k + 1) * kTerms + e);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mma_16816(d[i], a.x, a.y, a.z, a.w, y.v[i].z, y.v[i].w);
-    }
-  }
-}
 
 // Tile statistics of a row of a block whose quarter m is spread over the warp
 // as v[m] (-inf past the slice's end).
@@ -472,125 +443,312 @@ __device__ __forceinline__ void few_rows(const ExpandArgs& p, int adapter, const
 // lane's sums are 4 consecutive ids of a row: column n of the i-th product of 8
 // is id 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.  The units of a CTA's
 // warps follow one another, so those of one adapter share its B in L1.
-template <int STEPS, int LANES>  // rank_steps (0: any even number), lanes of 8 ranks in few_rows
-__global__ void __launch_bounds__(kExpandWarps * 32, STEPS == 1 || STEPS == 2 ? 4 : 3)
-    adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
-  // u stays in registers for one or two steps, in shared memory for four
-  constexpr bool kInRegs = STEPS == 1 || STEPS == 2;
-  __shared__ uint4 u_shared[STEPS == 4 ? kExpandWarps : 1][STEPS == 4 ? 4 * kTerms : 1][STEPS == 4 ? 32 : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
+// 16 or 8 bytes to shared memory in the background (0 bytes read: zeros).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// What a warp has in flight: the 16 rows' logits and the B of 64 ids, a lane's
+// own parts of both, so that a lane waits for its own copies only.  B: 4 ranks
+// of an id's row to a copy (one step), or 8.
+template <int STEPS>
+struct ExpandStage {
+  static constexpr int kCopies = STEPS == 1 ? 8 : 8 * STEPS / 2;  // of B
+  static constexpr int kBytes = STEPS == 1 ? 8 : 16;              // of one
+  uint4 x[8][32];
+  typename std::conditional<STEPS == 1, uint2, uint4>::type b[kCopies][32];
+};
+constexpr int kStages = 2;
+template <int STEPS>
+constexpr size_t expand_smem() {
+  return kExpandWarps * kStages * sizeof(ExpandStage<STEPS>);
+}
+// CTAs that the stages and the registers let stand on an SM.
+constexpr int expand_ctas(int steps) { return steps == 1 ? 4 : steps == 2 ? 3 : 2; }
+
+// A warp's unit: its plan entry, and where its u is.
+struct WarpUnit {
+  const int32_t* entry;
+  const uint32_t* u;
+  int adapter, count, block0, last_block;
+  bool work;
+};
+__device__ __forceinline__ WarpUnit warp_unit(const ExpandArgs& p, int warp, int steps) {
+  WarpUnit w{};
   const int item = static_cast<int>(blockIdx.x % p.slot_ctas) * kExpandWarps + warp;
-  const int block0 = static_cast<int>(blockIdx.x / p.slot_ctas) * p.warp_blocks;
+  w.block0 = static_cast<int>(blockIdx.x / p.slot_ctas) * p.warp_blocks;
+  w.last_block = min(w.block0 + p.warp_blocks, p.S * p.B);
   const int tile = item / p.slots, slot = item - tile * p.slots;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tile >= p.tiles) return;
+  if (tile >= p.tiles) return w;
   const int32_t* plan = p.plan + tile * plan_ints(p.slots);
-  const int32_t* entry = plan + 4 + slot * (kPlanUnit + 3);
-  if (slot >= plan[0]) return;
-  const int adapter = entry[0];
-  if (adapter < 0 && p.in_place && p.stats == nullptr) return;  // the base logits stay as they are
-  const int last_block = min(block0 + p.warp_blocks, p.S * p.B);
-  const int steps = STEPS > 0 ? STEPS : rank_steps(p.rank);
-  if (adapter >= 0 && entry[1] <= kFewRows) {  // the whole warp's
-    const float* u_rows =
-        reinterpret_cast<const float*>(p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment);
-    constexpr int kAtOnce = LANES < 16 ? kFewRows : 1;  // as many as the registers hold
-    for (int c = 0; c < entry[1]; c += kAtOnce)
-      few_rows<LANES, kAtOnce>(p, adapter, entry + 4 + c, min(entry[1] - c, kAtOnce), u_rows + c * steps * 16, steps * 16,
-                               block0, last_block, lane);
+  if (slot >= plan[0]) return w;
+  w.entry = plan + 4 + slot * (kPlanUnit + 3);
+  w.adapter = w.entry[0];
+  w.count = w.entry[1];
+  w.u = p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment;
+  // (in place, rows without an adapter: the base logits stay as they are)
+  w.work = !(w.adapter < 0 && p.in_place && p.stats == nullptr);
+  return w;
+}
+
+// Steps' products of 64 ids, y: a lane's B of eight products (two steps'), a:
+// u's operands of the step.
+__device__ __forceinline__ void step_products(float (&d)[8][4], const uint4 (&a)[kTerms], const uint2 (&y)[8]) {
+#pragma unroll
+  for (int e = 0; e < kTerms; ++e)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mma_16816(d[i], a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
+}
+
+// The sums of 64 ids onto a row's logits: -inf past the slice's end.
+__device__ __forceinline__ void add_sums(float4 (&x)[2][4], const float (&d)[8][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      x[i][b].x += d[2 * b][2 * i];
+      x[i][b].y += d[2 * b][2 * i + 1];
+      x[i][b].z += d[2 * b + 1][2 * i];
+      x[i][b].w += d[2 * b + 1][2 * i + 1];
+    }
+}
+
+// A warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice),
+// 64 ids at a time, the next 64's logits and B on their way meanwhile.  The
+// products' N index is laid over the ids so that a lane's sums are 4
+// consecutive ids of a row: column n of the i-th product of 8 is id
+// 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.
+template <int STEPS, int LANES>  // rank_steps, lanes of 8 ranks in few_rows
+__global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
+    adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
+  extern __shared__ uint4 expand_stages[];
+  using Stage = ExpandStage<STEPS>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const WarpUnit w = warp_unit(p, warp, STEPS);
+  if (!w.work) return;
+  if (w.adapter >= 0 && w.count <= kFewRows) {  // the whole warp's
+    few_rows<LANES, kFewRows>(p, w.adapter, w.entry + 4, w.count, reinterpret_cast<const float*>(w.u), STEPS * 16,
+                              w.block0, w.last_block, lane);
     return;
   }
-  const int r[2] = {entry[4 + g], entry[4 + g + 8]};
-  const uint4* u = reinterpret_cast<const uint4*>(
-      p.u + (static_cast<size_t>(tile) * p.slots + slot) * steps * kTerms * kFragment) + lane;
-  uint4 u_reg[kInRegs ? STEPS * kTerms : 1];
-  if (adapter >= 0) {
-    if (kInRegs) {
+  Stage* stages = reinterpret_cast<Stage*>(expand_stages) + warp * kStages;
+  const int r[2] = {w.entry[4 + g], w.entry[4 + g + 8]};
+  const size_t row_at[2] = {static_cast<size_t>(max(r[0], 0)) * p.V_s, static_cast<size_t>(max(r[1], 0)) * p.V_s};
+  uint4 u[STEPS * kTerms];
+  if (w.adapter >= 0) {
 #pragma unroll
-      for (int i = 0; i < STEPS * kTerms; ++i) u_reg[i] = u[i * 32];
-    }
-    if (STEPS == 4) {
-#pragma unroll
-      for (int i = 0; i < 4 * kTerms; ++i) u_shared[warp][i][lane] = u[i * 32];  // a lane reads its own back
-    }
+    for (int i = 0; i < STEPS * kTerms; ++i) u[i] = reinterpret_cast<const uint4*>(w.u)[i * 32 + lane];
   }
   const int n_id = 4 * (g >> 1) + (g & 1);  // the id of this lane's column, within 16 ids, of an even product
-  constexpr int kLaneRanks = STEPS == 1 ? 4 : 8;  // of one load
-  int slice = block0 / p.B, in_slice = block0 - slice * p.B;
+  constexpr int kLaneRanks = Stage::kBytes / 2;
+  const int slice0 = w.block0 / p.B;
+  // the copies of half h (64 ids) of the warp's blocks
+  int load_slice = slice0, load_block = w.block0 - slice0 * p.B;
+  auto issue = [&](int h) {
+    Stage& st = stages[h % kStages];
+    const int jh = load_block * 128 + 64 * (h & 1);
+    const float* src = p.logits[load_slice];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int j = jh + 16 * b + 4 * t;
+        const bool valid = r[i] >= 0 && j < p.V_s;
+        copy_async<16>(smem_u32(&st.x[4 * i + b][lane]), valid ? src + row_at[i] + j : src, valid);
+      }
+    if (w.adapter >= 0) {
+      // ids past the slice's end take its last one's row instead (their sums are not kept)
+      const int most = p.V_s - 1 - jh;
+      const __nv_bfloat16* b = p.b[load_slice] + (static_cast<size_t>(w.adapter) * p.V_s + jh) * p.rank + kLaneRanks * t;
+#pragma unroll
+      for (int k = 0; k < Stage::kCopies / 8; ++k) {
+        const bool ranks_in = 32 * k + kLaneRanks * t < p.rank;  // past the rank: zeros
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = min(16 * (i >> 1) + 2 * (i & 1) + n_id, most);
+          copy_async<Stage::kBytes>(smem_u32(&st.b[8 * k + i][lane]), ranks_in ? b + j * p.rank + 32 * k : p.b[load_slice],
+                                    ranks_in);
+        }
+      }
+    }
+    copy_commit();
+    if ((h & 1) && ++load_block == p.B) {
+      load_block = 0;
+      ++load_slice;
+    }
+  };
+  const int halves = 2 * (w.last_block - w.block0);
+  issue(0);
+  int slice = slice0, in_slice = w.block0 - slice0 * p.B;
+  HalfStats stats[2];
 #pragma unroll 1
-  for (int block = block0; block < last_block; ++block, ++in_slice) {
-    if (in_slice == p.B) {
+  for (int h = 0; h < halves; ++h) {
+    if (h + 1 < halves) {
+      issue(h + 1);
+      copy_wait<1>();
+    } else {
+      copy_wait<0>();
+    }
+    const Stage& st = stages[h % kStages];
+    const int jh = in_slice * 128 + 64 * (h & 1);
+    float4 x[2][4];
+    float d[8][4] = {};
+    if (w.adapter >= 0) {
+      if constexpr (STEPS == 1) {
+        uint2 y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = st.b[i][lane];
+        const uint4 a[kTerms] = {u[0], u[1], u[2]};
+        step_products(d, a, y);
+      } else {
+#pragma unroll
+        for (int k = 0; k < STEPS; k += 2) {
+          uint2 y[2][8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = st.b[4 * k + i][lane];
+            y[0][i] = make_uint2(v.x, v.y);
+            y[1][i] = make_uint2(v.z, v.w);
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint4 a[kTerms] = {u[(k + q) * kTerms], u[(k + q) * kTerms + 1], u[(k + q) * kTerms + 2]};
+            step_products(d, a, y[q]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint4 v = st.x[4 * i + b][lane];
+        x[i][b] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+      }
+    if (w.adapter >= 0) add_sums(x, d);
+    float* dst = p.out[slice];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int j = jh + 16 * b + 4 * t;
+        if (r[i] >= 0 && j < p.V_s)
+          *reinterpret_cast<float4*>(dst + row_at[i] + j) = x[i][b];
+        else
+          x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      }
+    if (p.stats != nullptr) {
+      const HalfStats now[2] = {half_stats(x[0]), half_stats(x[1])};
+      if (h & 1) {
+        const int block = w.block0 + (h >> 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (r[i] >= 0 && t == 0)
+            write_stats(stats[i], now[i], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
+      }
+      stats[0] = now[0];
+      stats[1] = now[1];
+    }
+    if ((h & 1) && ++in_slice == p.B) {
       in_slice = 0;
       ++slice;
     }
-    const int j0 = in_slice * 128;
-    const size_t base[2] = {static_cast<size_t>(r[0]) * p.V_s + j0 + 4 * t,
-                            static_cast<size_t>(r[1]) * p.V_s + j0 + 4 * t};
-    const float* src = p.logits[slice];
-    float* dst = p.out[slice];
-    HalfStats stats[2][2];
+  }
+}
+
+// The same for ranks above 64: B and u are loaded as they are used.
+template <int LANES>
+__global__ void __launch_bounds__(kExpandWarps * 32, 3) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int steps = rank_steps(p.rank);
+  const WarpUnit w = warp_unit(p, warp, steps);
+  if (!w.work) return;
+  if (w.adapter >= 0 && w.count <= kFewRows) {  // the whole warp's; a row at a time, as many as the registers hold
+    for (int c = 0; c < w.count; ++c)
+      few_rows<LANES, 1>(p, w.adapter, w.entry + 4 + c, 1, reinterpret_cast<const float*>(w.u) + c * steps * 16, steps * 16,
+                         w.block0, w.last_block, lane);
+    return;
+  }
+  const int r[2] = {w.entry[4 + g], w.entry[4 + g + 8]};
+  const size_t row_at[2] = {static_cast<size_t>(max(r[0], 0)) * p.V_s, static_cast<size_t>(max(r[1], 0)) * p.V_s};
+  const uint4* u = reinterpret_cast<const uint4*>(w.u) + lane;
+  const int n_id = 4 * (g >> 1) + (g & 1);
+  int slice = w.block0 / p.B, in_slice = w.block0 - slice * p.B;
+  HalfStats stats[2];
+#pragma unroll 1
+  for (int h = 0; h < 2 * (w.last_block - w.block0); ++h) {
+    const int jh = in_slice * 128 + 64 * (h & 1);
+    float4 x[2][4];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int jh = j0 + 64 * half;
-      float4 x[2][4];
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int b = 0; b < 4; ++b) {
+        const int j = jh + 16 * b + 4 * t;
+        x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (r[i] >= 0 && j < p.V_s) x[i][b] = *reinterpret_cast<const float4*>(p.logits[slice] + row_at[i] + j);
+      }
+    if (w.adapter >= 0) {
+      const int most = p.V_s - 1 - jh;
+      const __nv_bfloat16* b_base = p.b[slice] + (static_cast<size_t>(w.adapter) * p.V_s + jh) * p.rank + 8 * t;
+      float d[8][4] = {};
+#pragma unroll 1
+      for (int k = 0; k < steps; k += 2) {
+        uint2 y[2][8];
+        const bool ranks_in = 16 * k + 8 * t < p.rank;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int i = 0; i < 8; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (ranks_in) load_b(v, b_base + min(16 * (i >> 1) + 2 * (i & 1) + n_id, most) * p.rank + 16 * k);
+          y[0][i] = make_uint2(v.x, v.y);
+          y[1][i] = make_uint2(v.z, v.w);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint4* a_at = u + (k + q) * kTerms * 32;
+          const uint4 a[kTerms] = {a_at[0], a_at[32], a_at[64]};
+          step_products(d, a, y[q]);
+        }
+      }
+      add_sums(x, d);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int j = jh + 16 * b + 4 * t;
+        if (r[i] >= 0 && j < p.V_s)
+          *reinterpret_cast<float4*>(p.out[slice] + row_at[i] + j) = x[i][b];
+        else
           x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
-            x[i][b] = *reinterpret_cast<const float4*>(src + base[i] + 64 * half + 16 * b);
-        }
-      if (adapter >= 0) {
-        // ids past the slice's end read its last one's row instead (their sums are not kept)
-        const int most = p.V_s - 1 - jh;
-        const __nv_bfloat16* b_base = p.b[slice] + (static_cast<size_t>(adapter) * p.V_s + jh) * p.rank + kLaneRanks * t;
-        float d[8][4] = {};
-#pragma unroll
-        for (int k = 0; k < steps; k += STEPS == 1 ? 1 : 2) {
-          BLoad<STEPS> y;
-          const bool ranks_in = 16 * k + kLaneRanks * t < p.rank;  // past the rank: zeros
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int j = min(16 * (i >> 1) + 2 * (i & 1) + n_id, most);
-            y.v[i] = {};
-            if (ranks_in) load_b(y.v[i], b_base + j * p.rank + 16 * k);
-          }
-#pragma unroll
-          for (int e = 0; e < kTerms; ++e) {
-            const uint4 a = operand<STEPS>(u_reg, u_shared, u, warp, lane, k * kTerms + e);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mma_16816(d[i], a.x, a.y, a.z, a.w, y.v[i].x, y.v[i].y);
-          }
-          second_step<STEPS>(d, y, u_reg, u_shared, u, warp, lane, k);
-        }
+      }
+    if (p.stats != nullptr) {
+      const HalfStats now[2] = {half_stats(x[0]), half_stats(x[1])};
+      if (h & 1) {
+        const int block = w.block0 + (h >> 1);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            x[i][b].x += d[2 * b][2 * i];
-            x[i][b].y += d[2 * b][2 * i + 1];
-            x[i][b].z += d[2 * b + 1][2 * i];
-            x[i][b].w += d[2 * b + 1][2 * i + 1];
-          }
+          if (r[i] >= 0 && t == 0)
+            write_stats(stats[i], now[i], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (r[i] >= 0 && jh + 16 * b + 4 * t < p.V_s)
-            *reinterpret_cast<float4*>(dst + base[i] + 64 * half + 16 * b) = x[i][b];
-      if (p.stats != nullptr) {
-        stats[0][half] = half_stats(x[0]);
-        stats[1][half] = half_stats(x[1]);
-      }
+      stats[0] = now[0];
+      stats[1] = now[1];
     }
-    if (p.stats != nullptr && t == 0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (r[i] >= 0)
-          write_stats(stats[i][0], stats[i][1], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
+    if ((h & 1) && ++in_slice == p.B) {
+      in_slice = 0;
+      ++slice;
     }
   }
 }
@@ -612,13 +770,14 @@ AdapterSizes adapter_sizes(int R, int n, int rank) {
   return z;
 }
 
-template <typename Args>
-cudaError_t launch_after(void (*kernel)(Args), const Args& a, unsigned grid, cudaStream_t stream) {
-  // may start before the kernel ahead of it ends; waits for its results itself
+// The second kernel: may start before the one ahead of it ends, waits for its
+// results itself.
+cudaError_t launch_after(void (*kernel)(ExpandArgs), const ExpandArgs& a, unsigned grid, size_t smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kExpandWarps * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -626,6 +785,30 @@ cudaError_t launch_after(void (*kernel)(Args), const Args& a, unsigned grid, cud
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The shared-memory attributes of the second kernel's variants, once per
+// device, with it current.
+cudaError_t prepare_expand() {
+  constexpr int kMaxDevices = 64;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t status[kMaxDevices];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    const auto allow = [&](void (*kernel)(ExpandArgs), size_t smem) {
+      if (status[dev] == cudaSuccess)
+        status[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    };
+    status[dev] = cudaSuccess;
+    allow(adapters_expand_kernel<1, 1>, expand_smem<1>());
+    allow(adapters_expand_kernel<1, 2>, expand_smem<1>());
+    allow(adapters_expand_kernel<2, 4>, expand_smem<2>());
+    allow(adapters_expand_kernel<4, 8>, expand_smem<4>());
+  });
+  return status[dev];
 }
 
 }  // namespace
@@ -700,13 +883,15 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   const long long grid =
       static_cast<long long>(ea.slot_ctas) * ((static_cast<long long>(S) * ea.B + ea.warp_blocks - 1) / ea.warp_blocks);
   if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  auto kernel = rank <= 8     ? adapters_expand_kernel<1, 1>
-                : rank <= 16  ? adapters_expand_kernel<1, 2>
-                : rank <= 32  ? adapters_expand_kernel<2, 4>
-                : rank <= 64  ? adapters_expand_kernel<4, 8>
-                : rank <= 128 ? adapters_expand_kernel<0, 16>
-                              : adapters_expand_kernel<0, 32>;
-  return launch_after(kernel, ea, static_cast<unsigned>(grid), stream);
+  const unsigned g = static_cast<unsigned>(grid);
+  if (rank > 128) return launch_after(adapters_expand_wide_kernel<32>, ea, g, 0, stream);
+  if (rank > 64) return launch_after(adapters_expand_wide_kernel<16>, ea, g, 0, stream);
+  const cudaError_t e = prepare_expand();
+  if (e != cudaSuccess) return e;
+  if (rank > 32) return launch_after(adapters_expand_kernel<4, 8>, ea, g, expand_smem<4>(), stream);
+  if (rank > 16) return launch_after(adapters_expand_kernel<2, 4>, ea, g, expand_smem<2>(), stream);
+  if (rank > 8) return launch_after(adapters_expand_kernel<1, 2>, ea, g, expand_smem<1>(), stream);
+  return launch_after(adapters_expand_kernel<1, 1>, ea, g, expand_smem<1>(), stream);
 }
 
 }  // namespace vsl
