@@ -2,8 +2,10 @@
 
 A thin binding over the C ABI of ``libvsl.so`` (``include/vsl.h``): argument
 marshalling only; every step of the path runs in the library's CUDA kernels.
-PyTorch is used for device memory and streams.  There is no fallback: if the
-library is missing, importing the binding raises.
+PyTorch is used for device memory and streams.  The calls that score tokens
+and add adapters marshal in compiled code (``_binding.so``): their kernels take
+a few microseconds at the smallest sizes.  There is no fallback: if a library
+is missing, importing the binding raises.
 """
 import ctypes
 import os
@@ -120,6 +122,10 @@ def _load():
 
 
 lib = _load()
+
+from . import _binding  # noqa: E402  (after the library it calls)
+
+_binding.set_error_class(VslError)
 
 
 def status_string(status):
@@ -366,76 +372,16 @@ def verify_drafts(token_ids, draft_ids, token_logprob=None, out=None, stream=Non
     return out
 
 
-# Pointer arrays of up to MAX_SLICES entries (longer ones are refused by the library).
-_PTRS = [ctypes.c_void_p * n for n in range(MAX_SLICES + 2)]
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-def _addresses(ts):
-    return (_PTRS[len(ts)] if len(ts) < len(_PTRS) else ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
-
-
-def _slices(logits_slices, where):
-    """(R, S, V_s, device) of fp32 logits slices."""
-    first = logits_slices[0]
-    shape, dev = first.shape, first.device
-    R, V_s = shape
-    for t in logits_slices:
-        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{where}: logits slices must be contiguous fp32 [R, V_s] on one device")
-    return R, len(logits_slices), V_s, dev
-
-
-def _rows(t, name, dtype, shape, dev):
-    """Checks a per-row tensor (None passes)."""
-    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev):
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {dev}")
-    return t
-
-
-def _addr(t):
-    return t.data_ptr() if t is not None else None
-
-
-def _public_raw_stream(index):
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-# the current stream's handle without building a Stream object, where torch has the call
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
-
-
-def _call(function, where, dev, stream, *args):
-    """Calls the library with the tensors' device current, on ``stream`` (None: that device's current one)."""
-    if dev.type != "cuda":
-        raise ValueError(f"libvsl needs CUDA tensors, got a tensor on {dev}")
-    handle = _raw_stream(dev.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        status = function(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            status = function(*args, handle)
-    if status != 0:
-        raise VslError(status, where)
-
-
-def _grad_slices(grad, grad_dtype, R, S, V_s, dev):
-    """The gradient's slices (allocated when not given) and their VSL_GRAD_* type."""
-    if grad is None:
-        if grad_dtype is not torch.float32 and grad_dtype is not torch.bfloat16:
-            raise TypeError("the gradient is float32 or bfloat16")
-        if R * V_s % 8 == 0:  # every slice of one allocation is 16-byte aligned
-            grad = list(torch.empty(S, R, V_s, dtype=grad_dtype, device=dev).unbind(0))
-        else:
-            grad = [torch.empty(R, V_s, dtype=grad_dtype, device=dev) for _ in range(S)]
-        return grad, 1 if grad_dtype is torch.bfloat16 else 0
-    if len(grad) != S:
-        raise ValueError(f"grad must hold {S} slices")
-    dtype = grad[0].dtype
-    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+def _is_bf16(dtype):
+    if dtype is torch.bfloat16:
+        return True
+    if dtype is not torch.float32:
         raise TypeError("the gradient is float32 or bfloat16")
-    for t in grad:
-        _rows(t, "grad slices", dtype, (R, V_s), dev)
-    return grad, 1 if dtype is torch.bfloat16 else 0
+    return False
 
 
 def adapters_workspace_bytes(R, n_adapters, rank):
@@ -456,38 +402,12 @@ def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, ou
     ``adapters_workspace_bytes(R, n, rank)`` bytes (None: allocated for the call); calls that may run
     at the same time need one each.
     """
-    R, S, V_s, dev = _slices(logits_slices, "adapters_add")
-    n, rank, H = a.shape
-    bf16 = torch.bfloat16
-    if hidden.dtype is not bf16 or a.dtype is not bf16 or any(b.dtype is not bf16 for b in b_slices):
-        raise TypeError("hidden states and adapters must be bfloat16")
-    _rows(hidden, "hidden", bf16, (R, H), dev)
-    _rows(a, "a", bf16, (n, rank, H), dev)
-    if len(b_slices) != S:
-        raise ValueError(f"b_slices must hold {S} slices")
-    for b in b_slices:
-        _rows(b, "b_slices", bf16, (n, V_s, rank), dev)
-    _rows(adapter_ids, "adapter_ids", torch.int32, (R,), dev)
-    _rows(scale, "scale", torch.float32, (n,), dev)
-    if out is None:
-        out, _ = _grad_slices(None, torch.float32, R, S, V_s, dev)
-    if len(out) != S:
-        raise ValueError(f"out must hold {S} slices")
-    for t in out:
-        _rows(t, "out", torch.float32, (R, V_s), dev)
-    stats = None if tile_stats is None or tile_stats is False else _stats_tensor(tile_stats, R, S, V_s, dev)
-    if workspace is None:
-        size = lib.vsl_adapters_workspace_bytes(R, n, rank)
-        if stream is None or dev.type != "cuda":
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(stream):  # from the pool of the stream that uses it
-                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    _call(lib.vsl_adapters_add, "vsl_adapters_add", dev, stream, _addresses(logits_slices), _addresses(out),
-          hidden.data_ptr(), R, H, S, V_s, a.data_ptr(), _addresses(b_slices), _addr(scale), n, rank,
-          adapter_ids.data_ptr(), _addr(stats), workspace.data_ptr(), workspace.numel())
+    stats = None
+    if tile_stats is not None and tile_stats is not False:
+        R, V_s = logits_slices[0].shape
+        stats = _stats_tensor(tile_stats, R, len(logits_slices), V_s, logits_slices[0].device)
+    out = _binding.adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale, out, stats, workspace,
+                                _handle(stream))
     return out if stats is None else (out, stats)
 
 
@@ -509,21 +429,14 @@ def token_logprobs(logits_slices, token_ids, temperature=1.0, entropy=False, out
     logits_slices: list of fp32 [R, V_s] CUDA tensors; token_ids: int32 [R] (outside the vocabulary,
     -1 by convention: the row does not count, its outputs are 0).
     """
-    R, S, V_s, dev = _slices(logits_slices, "token_logprobs")
-    _rows(token_ids, "token_ids", torch.int32, (R,), dev)
     if out is None:
-        out = TokenLogprobs(torch.empty(R, device=dev), torch.empty(R, device=dev) if entropy else None,
-                            torch.empty(R, 2, device=dev), float(temperature))
-    else:
-        out.temperature = float(temperature)
-        _rows(out.logprob, "out.logprob", torch.float32, (R,), dev)
-        _rows(out.entropy, "out.entropy", torch.float32, (R,), dev)
-        _rows(out.row_stats, "out.row_stats", torch.float32, (R, 2), dev)
-        if entropy and out.entropy is None:
-            raise ValueError("out.entropy is missing")
-    _call(lib.vsl_token_logprobs, "vsl_token_logprobs", dev, stream, _addresses(logits_slices), R, S, V_s,
-          token_ids.data_ptr(), out.temperature, out.logprob.data_ptr(), _addr(out.entropy) if entropy else None,
-          out.row_stats.data_ptr())
+        return TokenLogprobs(*_binding.token_logprobs(logits_slices, token_ids, temperature, entropy, None, None, None,
+                                                      _handle(stream)), float(temperature))
+    if entropy and out.entropy is None:
+        raise ValueError("out.entropy is missing")
+    _binding.token_logprobs(logits_slices, token_ids, temperature, entropy, out.logprob, out.entropy, out.row_stats,
+                            _handle(stream))
+    out.temperature = float(temperature)
     return out
 
 
@@ -535,19 +448,9 @@ def token_logprobs_grad(logits_slices, token_ids, forward, d_logprob, d_entropy=
     when d_entropy is given); d_logprob, d_entropy: fp32 [R].  Returns the S slices [R, V_s] in
     ``grad_dtype`` (``grad`` if given; fp32 slices may be the logits themselves).
     """
-    R, S, V_s, dev = _slices(logits_slices, "token_logprobs_grad")
-    _rows(token_ids, "token_ids", torch.int32, (R,), dev)
-    _rows(forward.row_stats, "forward.row_stats", torch.float32, (R, 2), dev)
-    _rows(d_logprob, "d_logprob", torch.float32, (R,), dev)
-    _rows(d_entropy, "d_entropy", torch.float32, (R,), dev)
-    if d_entropy is not None and forward.entropy is None:
-        raise ValueError("d_entropy needs a forward call with entropy=True")
-    grad, kind = _grad_slices(grad, grad_dtype, R, S, V_s, dev)
-    ent = _rows(forward.entropy, "forward.entropy", torch.float32, (R,), dev) if d_entropy is not None else None
-    _call(lib.vsl_token_logprobs_grad, "vsl_token_logprobs_grad", dev, stream, _addresses(logits_slices), R, S, V_s,
-          token_ids.data_ptr(), forward.temperature, forward.row_stats.data_ptr(), _addr(ent), d_logprob.data_ptr(),
-          _addr(d_entropy), _addresses(grad), kind)
-    return grad
+    return _binding.token_logprobs_grad(logits_slices, token_ids, forward.temperature, forward.row_stats,
+                                        forward.entropy, d_logprob, d_entropy, grad, _is_bf16(grad_dtype),
+                                        _handle(stream))
 
 
 class PolicyLoss:
@@ -574,30 +477,10 @@ def policy_loss(logits_slices, token_ids, old_logprob, advantages, weights=None,
     grad: True (allocated in ``grad_dtype``), False / None (forward only) or S slices to fill (fp32
     slices may be the logits themselves).
     """
-    R, S, V_s, dev = _slices(logits_slices, "policy_loss")
-    _rows(token_ids, "token_ids", torch.int32, (R,), dev)
-    for t, name in ((old_logprob, "old_logprob"), (advantages, "advantages"), (weights, "weights"),
-                    (ref_logprob, "ref_logprob")):
-        _rows(t, name, torch.float32, (R,), dev)
-    kind = 0
-    if grad is True:
-        grad = None
-    elif grad is None or grad is False:
-        grad = False
-    if grad is not False:
-        grad, kind = _grad_slices(grad, grad_dtype, R, S, V_s, dev)
-    rows = torch.empty(4, R, device=dev).unbind(0)
-    out = PolicyLoss(*rows, grad if grad is not False else None)
-    i = _PolicyInputs(_addr(token_ids), _addr(old_logprob), _addr(advantages), _addr(ref_logprob), _addr(weights),
-                      clip_low, clip_high, kl_coef, entropy_coef, temperature)
-    at = rows[0].data_ptr()
-    o = _PolicyOutputs(at, at + 4 * R, at + 8 * R, at + 12 * R)
-    o.grad_type = kind
-    if out.grad is not None:
-        o.grad_slices = _addresses(out.grad)
-    _call(lib.vsl_policy_loss, "vsl_policy_loss", dev, stream, _addresses(logits_slices), R, S, V_s, ctypes.byref(i),
-          ctypes.byref(o))
-    return out
+    grad = None if grad is True else False if grad is None else grad
+    return PolicyLoss(*_binding.policy_loss(logits_slices, token_ids, old_logprob, advantages, weights, ref_logprob,
+                                            clip_low, clip_high, kl_coef, entropy_coef, temperature, grad,
+                                            _is_bf16(grad_dtype), _handle(stream)))
 
 
 class PreferenceLoss:
@@ -619,20 +502,8 @@ def preference_loss(logprob, ref_logprob, offsets, beta, label_smoothing=0.0, we
     logprob, ref_logprob (None: 0): fp32 [R]; offsets: int32 [2 * pairs + 1], non-decreasing, on the
     device; weights: fp32 [pairs].  ``d_logprob`` goes to ``token_logprobs_grad``.
     """
-    dev = logprob.device
-    R = logprob.numel()
-    pairs = (offsets.numel() - 1) // 2
-    _rows(logprob, "logprob", torch.float32, (R,), dev)
-    _rows(ref_logprob, "ref_logprob", torch.float32, (R,), dev)
-    if offsets.numel() < 3 or offsets.numel() % 2 == 0:
-        raise ValueError("offsets must hold 2 * pairs + 1 entries")
-    _rows(offsets, "offsets", torch.int32, (2 * pairs + 1,), dev)
-    _rows(weights, "weights", torch.float32, (pairs,), dev)
-    out = PreferenceLoss(torch.empty(pairs, device=dev), torch.empty(pairs, 2, device=dev), torch.empty(R, device=dev))
-    _call(lib.vsl_preference_loss, "vsl_preference_loss", dev, stream, logprob.data_ptr(), _addr(ref_logprob),
-          offsets.data_ptr(), _addr(weights), R, pairs, beta, label_smoothing, out.loss.data_ptr(),
-          out.rewards.data_ptr(), out.d_logprob.data_ptr())
-    return out
+    return PreferenceLoss(*_binding.preference_loss(logprob, ref_logprob, offsets, weights, beta, label_smoothing,
+                                                    _handle(stream)))
 
 
 def sample_launches(R, S, V_s):

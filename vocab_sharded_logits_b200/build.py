@@ -1,14 +1,18 @@
-"""Builds libvsl.so (the C-ABI library) in-tree with nvcc for sm_100a, and the
-test library tests/libvsl_test.so (the same objects plus the test-only probes
-of tests/csrc/vsl_test_probes.cu; never part of libvsl.so)."""
+"""Builds libvsl.so (the C-ABI library) in-tree with nvcc for sm_100a, the
+Python side of its shortest calls (_binding.so, g++ against torch's headers),
+and the test library tests/libvsl_test.so (the same objects plus the test-only
+probes of tests/csrc/vsl_test_probes.cu; never part of libvsl.so)."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libvsl.so")
+BINDING_SRC = os.path.join(CSRC, "vsl_binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 TEST_SRC = os.path.join(ROOT, "tests", "csrc", "vsl_test_probes.cu")
 TEST_LIB_PATH = os.path.join(ROOT, "tests", "libvsl_test.so")
 SOURCES = ["vsl_api.cu", "vsl_gemm.cu", "vsl_sample.cu", "vsl_verify.cu", "vsl_processed.cu", "vsl_tiles.cu",
@@ -23,9 +27,10 @@ def _nvcc():
 
 
 def needs_build():
-    if not os.path.exists(LIB_PATH) or not os.path.exists(TEST_LIB_PATH):
+    built = (LIB_PATH, TEST_LIB_PATH, BINDING_PATH)
+    if not all(os.path.exists(p) for p in built):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TEST_LIB_PATH))
+    t = min(os.path.getmtime(p) for p in built)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps += [os.path.join(ROOT, "include", "vsl.h"), TEST_SRC]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
@@ -44,8 +49,25 @@ def _link(objs, path):
     os.replace(tmp, path)
 
 
+def _build_binding(verbose):
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[x for p in include for x in ("-isystem", p)],
+           BINDING_SRC, "-o", tmp, "-L" + PKG_DIR, "-l:libvsl.so", "-L" + os.path.join(root, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force=False, verbose=False):
-    """Compile every CUDA source and link libvsl.so next to this file (and the test library)."""
+    """Compile every CUDA source, link libvsl.so next to this file (and the test library), and compile the binding."""
     if not force and not needs_build():
         return LIB_PATH
     objdir = os.path.join(ROOT, "_build")
@@ -56,6 +78,7 @@ def build(force=False, verbose=False):
         _compile(os.path.join(CSRC, src), obj, verbose)
         objs.append(obj)
     _link(objs, LIB_PATH)
+    _build_binding(verbose)
     probe = os.path.join(objdir, "vsl_test_probes.o")
     _compile(TEST_SRC, probe, verbose)
     _link(objs + [probe], TEST_LIB_PATH)

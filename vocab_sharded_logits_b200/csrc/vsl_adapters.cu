@@ -443,12 +443,15 @@ __device__ __forceinline__ void few_rows(const ExpandArgs& p, int adapter, const
 // lane's sums are 4 consecutive ids of a row: column n of the i-th product of 8
 // is id 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.  The units of a CTA's
 // warps follow one another, so those of one adapter share its B in L1.
-// 16 or 8 bytes to shared memory in the background (0 bytes read: zeros).
-template <int BYTES>
+// 16 or 8 bytes to shared memory in the background (not valid: zeros, nothing
+// read).  SHARED: through L1, where other warps of the SM find them.
+template <int BYTES, bool SHARED>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? BYTES : 0;
-  if constexpr (BYTES == 16)
+  if constexpr (!SHARED)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else if constexpr (BYTES == 16)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -554,33 +557,43 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
   const int n_id = 4 * (g >> 1) + (g & 1);  // the id of this lane's column, within 16 ids, of an even product
   constexpr int kLaneRanks = Stage::kBytes / 2;
   const int slice0 = w.block0 / p.B;
+  int at[8];  // B: where this lane's ids of 64 begin, in ranks
+#pragma unroll
+  for (int i = 0; i < 8; ++i) at[i] = (16 * (i >> 1) + 2 * (i & 1) + n_id) * p.rank + kLaneRanks * t;
+  bool ranks_in[Stage::kCopies / 8];  // past the rank: zeros
+#pragma unroll
+  for (int k = 0; k < Stage::kCopies / 8; ++k) ranks_in[k] = 32 * k + kLaneRanks * t < p.rank;
   // the copies of half h (64 ids) of the warp's blocks
   int load_slice = slice0, load_block = w.block0 - slice0 * p.B;
   auto issue = [&](int h) {
     Stage& st = stages[h % kStages];
     const int jh = load_block * 128 + 64 * (h & 1);
-    const float* src = p.logits[load_slice];
+    const bool whole = jh + 64 <= p.V_s;
+    const float* src = p.logits[load_slice] + jh + 4 * t;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      const float* row = src + row_at[i];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j = jh + 16 * b + 4 * t;
-        const bool valid = r[i] >= 0 && j < p.V_s;
-        copy_async<16>(smem_u32(&st.x[4 * i + b][lane]), valid ? src + row_at[i] + j : src, valid);
+      for (int b = 0; b < 4; ++b)
+        copy_async<16, false>(smem_u32(&st.x[4 * i + b][lane]), whole ? row + 16 * b : src - 4 * t - jh,
+                              r[i] >= 0 && whole);
+      if (!whole && r[i] >= 0) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (jh + 16 * b + 4 * t < p.V_s) copy_async<16, false>(smem_u32(&st.x[4 * i + b][lane]), row + 16 * b, true);
       }
+    }
     if (w.adapter >= 0) {
+      const __nv_bfloat16* b = p.b[load_slice] + (static_cast<size_t>(w.adapter) * p.V_s + jh) * p.rank;
       // ids past the slice's end take its last one's row instead (their sums are not kept)
-      const int most = p.V_s - 1 - jh;
-      const __nv_bfloat16* b = p.b[load_slice] + (static_cast<size_t>(w.adapter) * p.V_s + jh) * p.rank + kLaneRanks * t;
+      const int most = (p.V_s - 1 - jh) * p.rank + kLaneRanks * t;
 #pragma unroll
-      for (int k = 0; k < Stage::kCopies / 8; ++k) {
-        const bool ranks_in = 32 * k + kLaneRanks * t < p.rank;  // past the rank: zeros
+      for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat16* id = b + (whole ? at[i] : min(at[i], most));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = min(16 * (i >> 1) + 2 * (i & 1) + n_id, most);
-          copy_async<Stage::kBytes>(smem_u32(&st.b[8 * k + i][lane]), ranks_in ? b + j * p.rank + 32 * k : p.b[load_slice],
-                                    ranks_in);
-        }
+        for (int k = 0; k < Stage::kCopies / 8; ++k)
+          copy_async<Stage::kBytes, STEPS == 1>(smem_u32(&st.b[8 * k + i][lane]),
+                                                ranks_in[k] ? id + 32 * k : p.b[load_slice], ranks_in[k]);
       }
     }
     copy_commit();
