@@ -27,8 +27,10 @@ namespace vsl {
 
 namespace {
 
-constexpr int kThreads = 512;  // forward and gradient kernels
-constexpr int kPolicyCtas = 3; // CTAs of the policy kernel that stand on an SM
+constexpr int kThreads = 512;       // of a CTA
+constexpr int kSmallThreads = 128;  // of a CTA of the row kernels where a row has few logits
+constexpr int kSmallUnits = 2048;   // a row of at most so many units is one
+constexpr int kRowThreads = 1536;   // threads of the policy kernel that stand on an SM (40 registers each)
 constexpr int kBatch = 4;      // units of four logits a thread has in flight
 constexpr int kMaxCluster = 8;
 
@@ -202,7 +204,16 @@ __device__ __forceinline__ void add_at_token(const GradCoef& k, int i, float4& g
 __device__ __forceinline__ float4 unit_grad(const float4& x, const GradCoef& k, const ExpScale& c, int i) {
   const float v[4] = {x.x, x.y, x.z, x.w};
   float g[4];
-  if (!k.careful) {
+  if (!k.careful && k.gamma == 0.0f) {  // no entropy in it: alpha e_j
+    const float2 cc = make_float2(c.c, c.c), kk = make_float2(-k.ref, -k.ref), alpha = make_float2(k.alpha, k.alpha);
+    const float2 y0 = fma2(make_float2(x.x, x.y), cc, kk), y1 = fma2(make_float2(x.z, x.w), cc, kk);
+    const float2 g0 = mul2(make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), alpha);
+    const float2 g1 = mul2(make_float2(exp2_fast(y1.x), exp2_fast(y1.y)), alpha);
+    g[0] = g0.x;
+    g[1] = g0.y;
+    g[2] = g1.x;
+    g[3] = g1.y;
+  } else if (!k.careful) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float y = max_nan(__fmaf_rn(v[j], c.c, -k.ref), -200.0f);
@@ -222,7 +233,7 @@ __device__ __forceinline__ float4 unit_grad(const float4& x, const GradCoef& k, 
 
 // Gradient of units [first, last) of a row from global memory, a slice's run
 // at a time.
-template <typename T>
+template <typename T, int BATCH = kBatch>
 __device__ __forceinline__ void part_grad(const SliceArgs& a, const GradArgs& out, const GradCoef& k, int row,
                                           int first, int last, int thread, int threads) {
   SliceCursor run;
@@ -234,21 +245,21 @@ __device__ __forceinline__ void part_grad(const SliceArgs& a, const GradArgs& ou
     const size_t at = row_at + 4 * static_cast<size_t>(run.at);
     const float* src = a.slices[run.slice] + at;
     T* dst = static_cast<T*>(out.grad[run.slice]) + at;
-    for (int i = thread; i < n; i += kBatch * threads) {
-      float4 x[kBatch];
+    for (int i = thread; i < n; i += BATCH * threads) {
+      float4 x[BATCH];
       if (k.token >= 0) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+        for (int b = 0; b < BATCH; ++b)
           if (i + b * threads < n) x[b] = ldg_hint4(src + 4 * (i + b * threads), once);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+        for (int b = 0; b < BATCH; ++b)
           if (i + b * threads < n) x[b] = unit_grad(x[b], k, a.c, u + i + b * threads);
       } else {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int b = 0; b < BATCH; ++b) x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
+      for (int b = 0; b < BATCH; ++b)
         if (i + b * threads < n) store_unit(dst + 4 * (i + b * threads), x[b], once);
     }
     u += n;
@@ -269,9 +280,9 @@ struct LogprobArgs {
 
 // A cluster per row: each CTA streams a part of the row once; the CTAs exchange
 // their sums over distributed shared memory.
-template <bool ENT>
-__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  constexpr int kWarps = kThreads / 32;
+template <bool ENT, int THREADS>
+__global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+  constexpr int kWarps = THREADS / 32;
   __shared__ float first_max[kWarps];
   __shared__ float2 warps[kWarps];
   __shared__ CarefulSums careful_warps[kWarps];
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
   const float logit = warp == 0 ? token_logit(a.in, row, token) : 0.0f;
   const int first = min(a.in.units, rank * a.per_part), last = min(a.in.units, first + a.per_part);
   const uint64_t policy = policy_evict_first();
-  UnitReader reader(a.in, first, last, threadIdx.x, kThreads);
+  UnitReader reader(a.in, first, last, threadIdx.x, THREADS);
   float4 v[kBatch];
   reader.load(a.in, row, v, policy);
   float m = -FLT_MAX;
@@ -334,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
   }
   __syncthreads();
   if (!redo) return;  // the cluster's CTAs agree: they saw the same sums
-  careful_warp_sums(a.in, row, first, last, threadIdx.x, kThreads, careful_warps);
+  careful_warp_sums(a.in, row, first, last, threadIdx.x, THREADS, careful_warps);
   __syncthreads();
   if (warp == 0) {
     const PartStats p = careful_part(careful_warps, lane, kWarps, a.in.c);
@@ -364,7 +375,7 @@ struct LogprobGradArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) token_logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
   const int row = static_cast<int>(blockIdx.x) / a.parts;
   const int first = (static_cast<int>(blockIdx.x) - row * a.parts) * a.per_part;
   const int last = min(a.in.units, first + a.per_part);
@@ -378,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(const __g
     k = s.y < 0.0f ? grad_coef<false>(g, h, z, log(z), ent, 0.0, s.x, a.in.c, token)
                    : grad_coef<true>(g, h, z, log(z), ent, 0.0, s.x, a.in.c, token);
   }
-  part_grad<T>(a.in, a.out, k, row, first, last, threadIdx.x, kThreads);
+  part_grad<T, 2>(a.in, a.out, k, row, first, last, threadIdx.x, kThreads);
 }
 
 struct PolicyArgs {
@@ -452,13 +463,15 @@ __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int
   return grad_coef<FAST>(w * g, h, r.z, r.log_z, r.entropy, up, FAST ? ref : p.ref, a.in.c, token);
 }
 
-// A cluster per row.  Its CTAs stream the row once for the sums, exchange them
+// A cluster per row.  KEEP: its threads hold the row in registers between the
+// two passes.  Else its CTAs stream the row once for the sums, exchange them
 // over distributed shared memory, and read their parts again for the gradient,
 // out of the L2 cache: the first reading asks it to keep the lines, the second
 // and the gradient's stores to let theirs go first.
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
-  constexpr int kWarps = kThreads / 32;
+template <typename T, bool ENT, bool KEEP, int THREADS>
+__global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS)
+    policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
+  constexpr int kWarps = THREADS / 32;
   __shared__ float first_max[kWarps];
   __shared__ float2 warps[kWarps];
   __shared__ CarefulSums careful_warps[kWarps];
@@ -479,13 +492,13 @@ __global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_loss_kernel(cons
     }
     GradCoef off{};
     off.token = -1;
-    if (a.grad) part_grad<T>(a.in, a.out, off, row, first, last, threadIdx.x, kThreads);
+    if (a.grad) part_grad<T>(a.in, a.out, off, row, first, last, threadIdx.x, THREADS);
     return;
   }
   RowInputs in{};
   if (warp == 0) in = row_inputs(a, row, token);
-  const uint64_t keep = policy_evict_last();
-  UnitReader reader(a.in, first, last, threadIdx.x, kThreads);
+  const uint64_t keep = KEEP ? policy_evict_first() : policy_evict_last();
+  UnitReader reader(a.in, first, last, threadIdx.x, THREADS);
   float4 v[kBatch];
   reader.load(a.in, row, v, keep);
   float m = -FLT_MAX;
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_loss_kernel(cons
   FastSums s{};
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
-  while (reader.i < last) {
+  while (!KEEP && reader.i < last) {
     reader.load(a.in, row, v, keep);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
@@ -523,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_loss_kernel(cons
   }
   __syncthreads();
   if (redo) {  // the cluster's CTAs agree: they saw the same sums
-    careful_warp_sums(a.in, row, first, last, threadIdx.x, kThreads, careful_warps);
+    careful_warp_sums(a.in, row, first, last, threadIdx.x, THREADS, careful_warps);
     __syncthreads();
     if (warp == 0) {
       const PartStats p = careful_part(careful_warps, lane, kWarps, a.in.c);
@@ -537,7 +550,25 @@ __global__ void __launch_bounds__(kThreads, kPolicyCtas) policy_loss_kernel(cons
     }
     __syncthreads();
   }
-  if (a.grad) part_grad<T>(a.in, a.out, coef, row, first, last, threadIdx.x, kThreads);
+  if (!a.grad) return;
+  if (KEEP) {
+    const GradCoef g = coef;
+    const uint64_t once = policy_evict_first();
+    const int i0 = first + static_cast<int>(threadIdx.x);
+    SliceCursor at;
+    at.start(min(i0, a.in.units - 1), a.in.per_slice);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * THREADS;
+      if (i < last) {
+        store_unit(static_cast<T*>(a.out.grad[at.slice]) + static_cast<size_t>(row) * a.in.V_s + 4 * static_cast<size_t>(at.at),
+                   unit_grad(v[u], g, a.in.c, i), once);
+        if (i + THREADS < last) at.advance(THREADS, a.in.per_slice);
+      }
+    }
+  } else {
+    part_grad<T>(a.in, a.out, coef, row, first, last, threadIdx.x, THREADS);
+  }
 }
 
 SliceArgs slice_args(const float* const* logits, int S, int V_s, float temperature) {
@@ -566,42 +597,63 @@ cudaError_t device_sms(int* sms) {
   return status[dev];
 }
 
-// CTAs per row: as many as fill the SMs once (four to an SM), while a part
-// still has a unit or more per thread.
-cudaError_t row_cluster(int R, int units, int* cluster) {
+int row_threads(int units) { return units <= kSmallUnits ? kSmallThreads : kThreads; }
+
+// CTAs per row (a power of two): the fewest microseconds by a rough count.  The
+// SMs hold kRowThreads threads each, `places` CTAs in all; a full set of CTAs
+// takes `per_unit` for each unit a thread has, bound by memory, and `fixed` for
+// the steps that wait on one another; a last, partial set goes faster by its
+// share, but not faster than a third.  Both constants are fits to measured
+// times, and only their ratio matters: it keeps, say, 148 rows from taking 4
+// CTAs each, a third more than there are places (policy loss of 148 rows of
+// 151,936: 51 us with 4, 45 with 2).  `cached`: the rows being worked on at a
+// time must leave the L2 cache room, at most 96 MB of its 126 (2,048 rows of
+// 151,936: 0.50 ms with 4 CTAs a row, 67 MB; 0.55 with 2, 135 MB).
+cudaError_t choose_cluster(int R, int units, float per_unit, float fixed, bool cached, int* cluster) {
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  int c = 1;
-  while (c < kMaxCluster && static_cast<long long>(R) * c < 4LL * sms && units / (2 * c) >= kThreads) c *= 2;
-  if (static_cast<long long>(R) * c > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  *cluster = c;
-  return cudaSuccess;
+  const int threads = row_threads(units);
+  const float places = static_cast<float>(kRowThreads) * sms / threads;
+  float best = 0.0f;
+  *cluster = 0;
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
+    if (c > 1 && units / c < threads) break;  // a part has a unit or more per thread
+    const float sets = static_cast<float>(R) * c / places, whole = floorf(sets), rest = sets - whole;
+    const float rows = fminf(static_cast<float>(R), places / c);
+    if (cached && c < kMaxCluster && units / (2 * c) >= threads && rows * units * 16.0f > 96.0f * 1048576.0f) continue;
+    const float stream = per_unit * units / (static_cast<float>(c) * threads);
+    const float time = whole * (stream + fixed) + (rest > 0.0f ? stream * fmaxf(rest, 0.35f) + fixed : 0.0f);
+    if (*cluster == 0 || time < best) {
+      best = time;
+      *cluster = c;
+    }
+  }
+  return static_cast<long long>(R) * *cluster > 0x7FFFFFFFLL ? cudaErrorInvalidConfiguration : cudaSuccess;
 }
 
-// CTAs per row of the policy kernel: at least so many that the rows being
-// worked on at a time (kPolicyCtas CTAs to an SM) take at most 72 MB, which
-// the L2 cache keeps until their second reading (2,048 rows of 151,936: 0.50
-// ms with 4 CTAs a row, 67 MB; 0.55 with 2; 0.60 with 8, whose exchanges cost
-// more than the cache gives); more while there are fewer CTAs than places.
-cudaError_t policy_cluster(int R, int units, int* cluster) {
-  int sms = 0;
-  const cudaError_t e = device_sms(&sms);
+cudaError_t row_cluster(int R, int units, int* cluster) { return choose_cluster(R, units, 0.55f, 5.0f, false, cluster); }
+
+// keep: the threads hold their parts in registers between the two passes,
+// which pays where all CTAs run at once and time is latency (4 rows of 1,024:
+// 6.3 us, 8.4 without), not where it halves how many do (300 rows of 51,012: 73
+// us, 35 without).
+cudaError_t policy_cluster(int R, int units, int* cluster, bool* keep) {
+  const cudaError_t e = choose_cluster(R, units, 1.1f, 6.0f, true, cluster);
   if (e != cudaSuccess) return e;
-  int c = 1;
-  while (c < kMaxCluster && static_cast<long long>(kPolicyCtas) * sms / c * units * 16 > (72LL << 20)) c *= 2;
-  while (c < kMaxCluster && static_cast<long long>(R) * c < 1LL * kPolicyCtas * sms / 2 && units / (2 * c) >= kThreads) c *= 2;
-  if (static_cast<long long>(R) * c > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  *cluster = c;
+  int sms = 0;
+  const int threads = row_threads(units);
+  *keep = units <= *cluster * kBatch * threads && device_sms(&sms) == cudaSuccess &&
+          static_cast<long long>(R) * *cluster * threads <= 1024LL * sms;
   return cudaSuccess;
 }
 
 template <typename Args>
-cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, int R, int cluster, cudaStream_t stream) {
+cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, int R, int cluster, int threads, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   cfg.gridDim = dim3(static_cast<unsigned>(R) * cluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
@@ -611,6 +663,18 @@ cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, int R, int clus
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int THREADS>
+cudaError_t launch_policy(const PolicyArgs& a, int R, bool ent, bool keep, cudaStream_t stream) {
+  auto kernel = ent ? keep ? policy_loss_kernel<T, true, true, THREADS> : policy_loss_kernel<T, true, false, THREADS>
+                    : keep ? policy_loss_kernel<T, false, true, THREADS> : policy_loss_kernel<T, false, false, THREADS>;
+  return launch_clusters(kernel, a, R, a.cluster, THREADS, stream);
+}
+template <typename T>
+cudaError_t launch_policy(const PolicyArgs& a, int R, bool ent, bool keep, cudaStream_t stream) {
+  return row_threads(a.in.units) == kThreads ? launch_policy<T, kThreads>(a, R, ent, keep, stream)
+                                             : launch_policy<T, kSmallThreads>(a, R, ent, keep, stream);
 }
 
 }  // namespace
@@ -627,8 +691,12 @@ cudaError_t launch_token_logprobs(const float* const* logits, int R, int S, int 
   const cudaError_t e = row_cluster(R, a.in.units, &a.cluster);
   if (e != cudaSuccess) return e;
   a.per_part = (a.in.units + a.cluster - 1) / a.cluster;
-  return entropy != nullptr ? launch_clusters(token_logprobs_kernel<true>, a, R, a.cluster, stream)
-                            : launch_clusters(token_logprobs_kernel<false>, a, R, a.cluster, stream);
+  const bool ent = entropy != nullptr;
+  if (row_threads(a.in.units) == kThreads)
+    return launch_clusters(ent ? token_logprobs_kernel<true, kThreads> : token_logprobs_kernel<false, kThreads>, a, R,
+                           a.cluster, kThreads, stream);
+  return launch_clusters(ent ? token_logprobs_kernel<true, kSmallThreads> : token_logprobs_kernel<false, kSmallThreads>,
+                         a, R, a.cluster, kSmallThreads, stream);
 }
 
 cudaError_t launch_token_logprobs_grad(const float* const* logits, int R, int S, int V_s, const int32_t* token_ids,
@@ -675,15 +743,13 @@ cudaError_t launch_policy_loss(const float* const* logits, int R, int S, int V_s
   a.clip_high = in.clip_high;
   a.kl_coef = in.kl_coef;
   a.entropy_coef = in.entropy_coef;
-  const cudaError_t e = policy_cluster(R, a.in.units, &a.cluster);
+  bool keep = false;
+  const cudaError_t e = policy_cluster(R, a.in.units, &a.cluster, &keep);
   if (e != cudaSuccess) return e;
   a.per_part = (a.in.units + a.cluster - 1) / a.cluster;
   const bool ent = a.entropy != nullptr || a.entropy_coef != 0.0f;
-  if (out.grad_type == VSL_GRAD_BF16)
-    return ent ? launch_clusters(policy_loss_kernel<__nv_bfloat16, true>, a, R, a.cluster, stream)
-               : launch_clusters(policy_loss_kernel<__nv_bfloat16, false>, a, R, a.cluster, stream);
-  return ent ? launch_clusters(policy_loss_kernel<float, true>, a, R, a.cluster, stream)
-             : launch_clusters(policy_loss_kernel<float, false>, a, R, a.cluster, stream);
+  if (out.grad_type == VSL_GRAD_BF16) return launch_policy<__nv_bfloat16>(a, R, ent, keep, stream);
+  return launch_policy<float>(a, R, ent, keep, stream);
 }
 
 }  // namespace vsl
