@@ -65,6 +65,16 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 struct ShrinkArgs {
   const __nv_bfloat16* hidden;
   const __nv_bfloat16* a;
@@ -251,55 +261,83 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Tile statistics of half a block (64 ids) of a row: the row's 4 lanes (same g)
-// hold 8 logits of each of its two quarters (v[b] = ids 16 b + 4 t ..), -inf
-// past the slice's end.  Every lane of the four holds the result.
-struct HalfStats {
-  float q[2], sum, mn, am;
-};
-__device__ __forceinline__ HalfStats half_stats(const float4 (&v)[4]) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  HalfStats s;
-  s.mn = INFINITY;
-  s.am = INFINITY;
-  s.q[0] = s.q[1] = -INFINITY;
+// Tile statistics of a row of a block, a quarter (32 ids) after another: the
+// row's 4 lanes (same g) hold 8 logits of the quarter (v[b] = ids 16 b + 4 t ..),
+// -inf past the slice's end.  Sums and minima stay a lane's own until the end.
+
+// The largest of a lane's logits, the smallest finite one, the smallest nonzero
+// |l| (infinite ones count as +inf).
+template <int N>
+__device__ __forceinline__ void lane_extremes(const float (&x)[N], float& top, float& mn, float& am) {
+  top = x[0];
+  mn = x[0];
+  am = fabsf(x[0]);
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const float x[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+  for (int i = 1; i < N; ++i) {
+    top = fmaxf(top, x[i]);  // (NaN: dropped by all three)
+    mn = fminf(mn, x[i]);
+    am = fminf(am, fabsf(x[i]));
+  }
+  if (mn == -INFINITY || am == 0.0f || mn != mn) {  // rare: what does not count is among them
+    top = -INFINITY;
+    mn = INFINITY;
+    am = INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      s.q[b >> 1] = fmaxf(s.q[b >> 1], x[j]);
-      s.mn = fminf(s.mn, isfinite(x[j]) ? x[j] : INFINITY);
-      s.am = fminf(s.am, x[j] != 0.0f ? fabsf(x[j]) : INFINITY);
+    for (int i = 0; i < N; ++i) {
+      top = fmaxf(top, x[i]);
+      mn = fminf(mn, isfinite(x[i]) ? x[i] : INFINITY);
+      am = fminf(am, x[i] != 0.0f ? fabsf(x[i]) : INFINITY);
     }
   }
+}
+struct BlockStats {
+  float q[4], sum[4], mn, am;  // sum[i] relative to q[i] where that is finite
+};
+__device__ __forceinline__ void quarter_stats(BlockStats& s, int quarter, const float4 (&v)[2]) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  float top, mn, am;
+  lane_extremes(x, top, mn, am);
+  if (quarter != 0) {
+    mn = fminf(mn, s.mn);
+    am = fminf(am, s.am);
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  const float c = isfinite(top) ? top : 0.0f;
+  float sum = 0.0f;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+    sum += ex2((v[b].x - c) * kLog2e) + ex2((v[b].y - c) * kLog2e) + ex2((v[b].z - c) * kLog2e) +
+           ex2((v[b].w - c) * kLog2e);
+  s.mn = mn;
+  s.am = am;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // static registers
+    if (i == quarter) {
+      s.q[i] = top;
+      s.sum[i] = sum;
+    }
+}
+// By all lanes of the warp; the row's first one writes.
+__device__ __forceinline__ void write_stats(const BlockStats& s, float* rec, bool write) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float top = fmaxf(fmaxf(s.q[0], s.q[1]), fmaxf(s.q[2], s.q[3]));
+  const float c = isfinite(top) ? top : 0.0f;
+  float sum = 0.0f, mn = s.mn, am = s.am;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // a quarter without a finite maximum has the sum 0, +inf or NaN whatever it is relative to
+    sum += s.sum[i] * (isfinite(s.q[i]) ? ex2((s.q[i] - c) * kLog2e) : 1.0f);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    s.q[0] = fmaxf(s.q[0], __shfl_xor_sync(0xFFFFFFFFu, s.q[0], o));
-    s.q[1] = fmaxf(s.q[1], __shfl_xor_sync(0xFFFFFFFFu, s.q[1], o));
-    s.mn = fminf(s.mn, __shfl_xor_sync(0xFFFFFFFFu, s.mn, o));
-    s.am = fminf(s.am, __shfl_xor_sync(0xFFFFFFFFu, s.am, o));
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    mn = fminf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
+    am = fminf(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
   }
-  const float top = fmaxf(s.q[0], s.q[1]);
-  const float c = isfinite(top) ? top : 0.0f;
-  s.sum = 0.0f;
-#pragma unroll
-  for (int b = 0; b < 4; ++b)
-    s.sum += ex2((v[b].x - c) * kLog2e) + ex2((v[b].y - c) * kLog2e) + ex2((v[b].z - c) * kLog2e) +
-             ex2((v[b].w - c) * kLog2e);
-  s.sum += __shfl_xor_sync(0xFFFFFFFFu, s.sum, 1);
-  s.sum += __shfl_xor_sync(0xFFFFFFFFu, s.sum, 2);
-  return s;
-}
-__device__ __forceinline__ void write_stats(const HalfStats& a, const HalfStats& b, float* rec) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float ta = fmaxf(a.q[0], a.q[1]), tb = fmaxf(b.q[0], b.q[1]), top = fmaxf(ta, tb);
-  const float c = isfinite(top) ? top : 0.0f;
-  // a half without a finite maximum has the sum 0, +inf or NaN whatever it is taken relative to
-  const float sum = a.sum * (isfinite(ta) ? ex2((ta - c) * kLog2e) : 1.0f) +
-                    b.sum * (isfinite(tb) ? ex2((tb - c) * kLog2e) : 1.0f);
-  reinterpret_cast<float4*>(rec)[0] = make_float4(a.q[0], a.q[1], b.q[0], b.q[1]);
-  reinterpret_cast<float4*>(rec)[1] = make_float4(sum, fminf(a.mn, b.mn), fminf(a.am, b.am), 0.0f);
+  if (write) {
+    reinterpret_cast<float4*>(rec)[0] = make_float4(s.q[0], s.q[1], s.q[2], s.q[3]);
+    reinterpret_cast<float4*>(rec)[1] = make_float4(sum, mn, am, 0.0f);
+  }
 }
 
 __device__ __forceinline__ void load_b(uint4& v, const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
@@ -438,22 +476,25 @@ __device__ __forceinline__ void few_rows(const ExpandArgs& p, int adapter, const
   }
 }
 
-// A warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice),
-// 64 ids at a time.  The products' N index is laid over the ids so that a
-// lane's sums are 4 consecutive ids of a row: column n of the i-th product of 8
-// is id 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.  The units of a CTA's
-// warps follow one another, so those of one adapter share its B in L1.
-// 16 or 8 bytes to shared memory in the background (not valid: zeros, nothing
-// read).  SHARED: through L1, where other warps of the SM find them.
-template <int BYTES, bool SHARED>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? BYTES : 0;
-  if constexpr (!SHARED)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else if constexpr (BYTES == 16)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// 16 or 8 bytes from src + FROM to shared memory at dst + TO, in the
+// background.  16: past L1; 8: through it.
+template <int BYTES, int TO, int FROM>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(TO), "n"(FROM) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %3], 8;" ::"r"(dst), "l"(src), "n"(TO), "n"(FROM) : "memory");
+}
+// The same where `valid`, else zeros (nothing is read).
+template <int BYTES, int TO, int FROM>
+__device__ __forceinline__ void copy_async_or_zero(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16, %4;" ::"r"(dst), "l"(src), "n"(TO), "n"(FROM), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0 + %2], [%1 + %3], 8, %4;" ::"r"(dst), "l"(src), "n"(TO), "n"(FROM), "r"(n)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -461,23 +502,23 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-// What a warp has in flight: the 16 rows' logits and the B of 64 ids, a lane's
-// own parts of both, so that a lane waits for its own copies only.  B: 4 ranks
-// of an id's row to a copy (one step), or 8.
+// What a warp has in flight: the 16 rows' logits and the B of a quarter (32
+// ids), a lane's own parts of both, so that a lane waits for its own copies
+// only.  B: 4 ranks of an id's row to a copy (one step), or 8.
 template <int STEPS>
 struct ExpandStage {
-  static constexpr int kCopies = STEPS == 1 ? 8 : 8 * STEPS / 2;  // of B
+  static constexpr int kCopies = STEPS == 1 ? 4 : 4 * STEPS / 2;  // of B
   static constexpr int kBytes = STEPS == 1 ? 8 : 16;              // of one
-  uint4 x[8][32];
+  uint4 x[4][32];
   typename std::conditional<STEPS == 1, uint2, uint4>::type b[kCopies][32];
 };
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 template <int STEPS>
 constexpr size_t expand_smem() {
   return kExpandWarps * kStages * sizeof(ExpandStage<STEPS>);
 }
 // CTAs that the stages and the registers let stand on an SM.
-constexpr int expand_ctas(int steps) { return steps == 1 ? 4 : steps == 2 ? 3 : 2; }
+constexpr int expand_ctas(int steps) { return steps == 4 ? 3 : 4; }
 
 // A warp's unit: its plan entry, and where its u is.
 struct WarpUnit {
@@ -505,21 +546,27 @@ __device__ __forceinline__ WarpUnit warp_unit(const ExpandArgs& p, int warp, int
   return w;
 }
 
-// Steps' products of 64 ids, y: a lane's B of eight products (two steps'), a:
-// u's operands of the step.
-__device__ __forceinline__ void step_products(float (&d)[8][4], const uint4 (&a)[kTerms], const uint2 (&y)[8]) {
+// A step's products of 32 ids: y, a lane's B of the four products; a, u's
+// operands of the step; FIRST: the sums begin with it.
+template <bool FIRST>
+__device__ __forceinline__ void step_products(float (&d)[4][4], const uint4 (&a)[kTerms], const uint2 (&y)[4]) {
 #pragma unroll
   for (int e = 0; e < kTerms; ++e)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mma_16816(d[i], a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
+    for (int i = 0; i < 4; ++i) {
+      if (FIRST && e == 0)
+        mma_16816_first(d[i], a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
+      else
+        mma_16816(d[i], a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
+    }
 }
 
-// The sums of 64 ids onto a row's logits: -inf past the slice's end.
-__device__ __forceinline__ void add_sums(float4 (&x)[2][4], const float (&d)[8][4]) {
+// The sums of 32 ids onto the rows' logits.
+__device__ __forceinline__ void add_sums(float4 (&x)[2][2], const float (&d)[4][4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 2; ++b) {
       x[i][b].x += d[2 * b][2 * i];
       x[i][b].y += d[2 * b][2 * i + 1];
       x[i][b].z += d[2 * b + 1][2 * i];
@@ -527,10 +574,26 @@ __device__ __forceinline__ void add_sums(float4 (&x)[2][4], const float (&d)[8][
     }
 }
 
-// A warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice),
-// 64 ids at a time, the next 64's logits and B on their way meanwhile.  The
-// products' N index is laid over the ids so that a lane's sums are 4
-// consecutive ids of a row: column n of the i-th product of 8 is id
+// Stores a quarter of the unit's rows, j its first id; a lane's logits past the
+// slice's end become -inf (for the statistics).
+__device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)[2], const int (&r)[2], int j, int V_s,
+                                              int t, float4 (&x)[2][2]) {
+  dst += j + 4 * t;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (j + 16 * b + 4 * t >= V_s)
+        x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      else if (r[i] >= 0)
+        *reinterpret_cast<float4*>(dst + row_at[i] + 16 * b) = x[i][b];
+    }
+}
+
+// A warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice), a
+// quarter at a time, the next quarters' logits and B on their way meanwhile.
+// The products' N index is laid over the ids so that a lane's sums are 4
+// consecutive ids of a row: column n of the i-th product of 4 is id
 // 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.
 template <int STEPS, int LANES>  // rank_steps, lanes of 8 ranks in few_rows
 __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
@@ -557,124 +620,146 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
   const int n_id = 4 * (g >> 1) + (g & 1);  // the id of this lane's column, within 16 ids, of an even product
   constexpr int kLaneRanks = Stage::kBytes / 2;
   const int slice0 = w.block0 / p.B;
-  int at[8];  // B: where this lane's ids of 64 begin, in ranks
-#pragma unroll
-  for (int i = 0; i < 8; ++i) at[i] = (16 * (i >> 1) + 2 * (i & 1) + n_id) * p.rank + kLaneRanks * t;
-  bool ranks_in[Stage::kCopies / 8];  // past the rank: zeros
-#pragma unroll
-  for (int k = 0; k < Stage::kCopies / 8; ++k) ranks_in[k] = 32 * k + kLaneRanks * t < p.rank;
-  // the copies of half h (64 ids) of the warp's blocks
-  int load_slice = slice0, load_block = w.block0 - slice0 * p.B;
+  const bool even_ranks = p.rank == 16 * STEPS;
+  // this lane's places in what quarter h of the warp's blocks copies: two rows'
+  // logits, and the B of its ids, whose rows are 0, 2, 16 and 18 from the first
+  int load_slice = slice0, load_j = 128 * (w.block0 - slice0 * p.B);
+  const int two = 2 * p.rank;
+  const float *x0, *x1;
+  const __nv_bfloat16* b0;
+  auto place = [&] {
+    const float* src = p.logits[load_slice] + load_j + 4 * t;
+    x0 = src + row_at[0];
+    x1 = src + row_at[1];
+    b0 = p.b[load_slice] +
+         (static_cast<size_t>(w.adapter >= 0 ? w.adapter : 0) * p.V_s + load_j + n_id) * p.rank + kLaneRanks * t;
+  };
+  place();
   auto issue = [&](int h) {
     Stage& st = stages[h % kStages];
-    const int jh = load_block * 128 + 64 * (h & 1);
-    const bool whole = jh + 64 <= p.V_s;
-    const float* src = p.logits[load_slice] + jh + 4 * t;
+    const uint32_t x_to = smem_u32(&st.x[0][lane]), b_to = smem_u32(&st.b[0][lane]);
+    constexpr int kB = Stage::kBytes, kRow = 32 * kB;  // a copy over the warp's lanes
+    if (load_j + 32 <= p.V_s) {
+      if (r[0] >= 0) {
+        copy_async<16, 0, 0>(x_to, x0);
+        copy_async<16, 512, 64>(x_to, x0);
+      }
+      if (r[1] >= 0) {
+        copy_async<16, 1024, 0>(x_to, x1);
+        copy_async<16, 1536, 64>(x_to, x1);
+      }
+      if (w.adapter >= 0) {
+        const __nv_bfloat16* id[4] = {b0, b0 + two, b0 + 8 * two, b0 + 9 * two};
+        if (even_ranks) {
+          copy_async<kB, 0, 0>(b_to, id[0]);
+          copy_async<kB, kRow, 0>(b_to, id[1]);
+          copy_async<kB, 2 * kRow, 0>(b_to, id[2]);
+          copy_async<kB, 3 * kRow, 0>(b_to, id[3]);
+          if constexpr (STEPS == 4) {
+            copy_async<kB, 4 * kRow, 64>(b_to, id[0]);
+            copy_async<kB, 5 * kRow, 64>(b_to, id[1]);
+            copy_async<kB, 6 * kRow, 64>(b_to, id[2]);
+            copy_async<kB, 7 * kRow, 64>(b_to, id[3]);
+          }
+        } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* row = src + row_at[i];
+          for (int i = 0; i < 4; ++i) {  // past the rank: zeros
+            copy_async_or_zero<kB, 0, 0>(b_to + i * kRow, id[i], kLaneRanks * t < p.rank);
+            if constexpr (STEPS == 4) copy_async_or_zero<kB, 4 * kRow, 64>(b_to + i * kRow, id[i], 32 + 8 * t < p.rank);
+          }
+        }
+      }
+    } else {  // the slice's end
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        copy_async<16, false>(smem_u32(&st.x[4 * i + b][lane]), whole ? row + 16 * b : src - 4 * t - jh,
-                              r[i] >= 0 && whole);
-      if (!whole && r[i] >= 0) {
+      for (int q = 0; q < 2; ++q)
+        if (load_j + 16 * q + 4 * t < p.V_s) {
+          if (r[0] >= 0) copy_async<16, 0, 0>(x_to + q * 512, x0 + 16 * q);
+          if (r[1] >= 0) copy_async<16, 0, 0>(x_to + (2 + q) * 512, x1 + 16 * q);
+        }
+      if (w.adapter >= 0) {
+        // ids past it take its last one's row instead (their sums are not kept)
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (jh + 16 * b + 4 * t < p.V_s) copy_async<16, false>(smem_u32(&st.x[4 * i + b][lane]), row + 16 * b, true);
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat16* id = b0 + min(16 * (i >> 1) + 2 * (i & 1), p.V_s - 1 - load_j - n_id) * p.rank;
+          copy_async_or_zero<kB, 0, 0>(b_to + i * kRow, id, kLaneRanks * t < p.rank);
+          if constexpr (STEPS == 4) copy_async_or_zero<kB, 4 * kRow, 64>(b_to + i * kRow, id, 32 + 8 * t < p.rank);
+        }
       }
     }
-    if (w.adapter >= 0) {
-      const __nv_bfloat16* b = p.b[load_slice] + (static_cast<size_t>(w.adapter) * p.V_s + jh) * p.rank;
-      // ids past the slice's end take its last one's row instead (their sums are not kept)
-      const int most = (p.V_s - 1 - jh) * p.rank + kLaneRanks * t;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __nv_bfloat16* id = b + (whole ? at[i] : min(at[i], most));
-#pragma unroll
-        for (int k = 0; k < Stage::kCopies / 8; ++k)
-          copy_async<Stage::kBytes, STEPS == 1>(smem_u32(&st.b[8 * k + i][lane]),
-                                                ranks_in[k] ? id + 32 * k : p.b[load_slice], ranks_in[k]);
-      }
-    }
-    copy_commit();
-    if ((h & 1) && ++load_block == p.B) {
-      load_block = 0;
-      ++load_slice;
+    load_j += 32;
+    x0 += 32;
+    x1 += 32;
+    b0 += 16 * two;
+    if ((h & 3) == 3 && load_j >= p.V_s && ++load_slice < p.S) {  // (the last slice's end: no more is issued)
+      load_j = 0;
+      place();
     }
   };
-  const int halves = 2 * (w.last_block - w.block0);
-  issue(0);
+  const int quarters = 4 * (w.last_block - w.block0);
+#pragma unroll
+  for (int h = 0; h < kStages - 1; ++h) {
+    issue(h);  // (a warp has four quarters at least)
+    copy_commit();
+  }
   int slice = slice0, in_slice = w.block0 - slice0 * p.B;
-  HalfStats stats[2];
+  BlockStats stats[2];
 #pragma unroll 1
-  for (int h = 0; h < halves; ++h) {
-    if (h + 1 < halves) {
-      issue(h + 1);
-      copy_wait<1>();
-    } else {
-      copy_wait<0>();
-    }
+  for (int h = 0; h < quarters; ++h) {
+    if (h + kStages - 1 < quarters) issue(h + kStages - 1);
+    copy_commit();  // a group a quarter, empty ones at the end
+    copy_wait<kStages - 1>();
     const Stage& st = stages[h % kStages];
-    const int jh = in_slice * 128 + 64 * (h & 1);
-    float4 x[2][4];
-    float d[8][4] = {};
+    const int j = in_slice * 128 + 32 * (h & 3);
+    float4 x[2][2];
+    float d[4][4];
     if (w.adapter >= 0) {
       if constexpr (STEPS == 1) {
-        uint2 y[8];
+        uint2 y[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = st.b[i][lane];
+        for (int i = 0; i < 4; ++i) y[i] = st.b[i][lane];
         const uint4 a[kTerms] = {u[0], u[1], u[2]};
-        step_products(d, a, y);
+        step_products<true>(d, a, y);
       } else {
 #pragma unroll
         for (int k = 0; k < STEPS; k += 2) {
-          uint2 y[2][8];
+          uint2 y0[4], y1[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 v = st.b[4 * k + i][lane];
-            y[0][i] = make_uint2(v.x, v.y);
-            y[1][i] = make_uint2(v.z, v.w);
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = st.b[2 * k + i][lane];
+            y0[i] = make_uint2(v.x, v.y);
+            y1[i] = make_uint2(v.z, v.w);
           }
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint4 a[kTerms] = {u[(k + q) * kTerms], u[(k + q) * kTerms + 1], u[(k + q) * kTerms + 2]};
-            step_products(d, a, y[q]);
-          }
+          const uint4 a0[kTerms] = {u[k * kTerms], u[k * kTerms + 1], u[k * kTerms + 2]};
+          const uint4 a1[kTerms] = {u[(k + 1) * kTerms], u[(k + 1) * kTerms + 1], u[(k + 1) * kTerms + 2]};
+          if (k == 0)
+            step_products<true>(d, a0, y0);
+          else
+            step_products<false>(d, a0, y0);
+          step_products<false>(d, a1, y1);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint4 v = st.x[4 * i + b][lane];
+      for (int b = 0; b < 2; ++b) {
+        const uint4 v = st.x[2 * i + b][lane];
         x[i][b] = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
       }
     if (w.adapter >= 0) add_sums(x, d);
-    float* dst = p.out[slice];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j = jh + 16 * b + 4 * t;
-        if (r[i] >= 0 && j < p.V_s)
-          *reinterpret_cast<float4*>(dst + row_at[i] + j) = x[i][b];
-        else
-          x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      }
+    store_quarter(p.out[slice], row_at, r, j, p.V_s, t, x);
     if (p.stats != nullptr) {
-      const HalfStats now[2] = {half_stats(x[0]), half_stats(x[1])};
-      if (h & 1) {
-        const int block = w.block0 + (h >> 1);
+      quarter_stats(stats[0], h & 3, x[0]);
+      quarter_stats(stats[1], h & 3, x[1]);
+      if ((h & 3) == 3) {
+        const int block = w.block0 + (h >> 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (r[i] >= 0 && t == 0)
-            write_stats(stats[i], now[i], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
+          write_stats(stats[i], p.stats + (static_cast<size_t>(max(r[i], 0)) * p.S * p.B + block) * 8,
+                      r[i] >= 0 && t == 0);
       }
-      stats[0] = now[0];
-      stats[1] = now[1];
     }
-    if ((h & 1) && ++in_slice == p.B) {
+    if ((h & 3) == 3 && ++in_slice == p.B) {
       in_slice = 0;
       ++slice;
     }
@@ -683,7 +768,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
 
 // The same for ranks above 64: B and u are loaded as they are used.
 template <int LANES>
-__global__ void __launch_bounds__(kExpandWarps * 32, 3) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
+__global__ void __launch_bounds__(kExpandWarps * 32, 4) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int steps = rank_steps(p.rank);
@@ -700,66 +785,53 @@ __global__ void __launch_bounds__(kExpandWarps * 32, 3) adapters_expand_wide_ker
   const uint4* u = reinterpret_cast<const uint4*>(w.u) + lane;
   const int n_id = 4 * (g >> 1) + (g & 1);
   int slice = w.block0 / p.B, in_slice = w.block0 - slice * p.B;
-  HalfStats stats[2];
+  BlockStats stats[2];
 #pragma unroll 1
-  for (int h = 0; h < 2 * (w.last_block - w.block0); ++h) {
-    const int jh = in_slice * 128 + 64 * (h & 1);
-    float4 x[2][4];
+  for (int h = 0; h < 4 * (w.last_block - w.block0); ++h) {
+    const int j = in_slice * 128 + 32 * (h & 3);
+    float4 x[2][2] = {};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j = jh + 16 * b + 4 * t;
-        x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (r[i] >= 0 && j < p.V_s) x[i][b] = *reinterpret_cast<const float4*>(p.logits[slice] + row_at[i] + j);
-      }
+      for (int b = 0; b < 2; ++b)
+        if (r[i] >= 0 && j + 16 * b + 4 * t < p.V_s)
+          x[i][b] = *reinterpret_cast<const float4*>(p.logits[slice] + row_at[i] + j + 16 * b + 4 * t);
     if (w.adapter >= 0) {
-      const int most = p.V_s - 1 - jh;
-      const __nv_bfloat16* b_base = p.b[slice] + (static_cast<size_t>(w.adapter) * p.V_s + jh) * p.rank + 8 * t;
-      float d[8][4] = {};
-#pragma unroll 1
+      const __nv_bfloat16* id0 = p.b[slice] + (static_cast<size_t>(w.adapter) * p.V_s + j + n_id) * p.rank + 8 * t;
+      const int most = p.V_s - 1 - j - n_id;  // ids past the slice's end take its last one's row instead
+      float d[4][4] = {};
+#pragma unroll 2
       for (int k = 0; k < steps; k += 2) {
-        uint2 y[2][8];
+        uint2 y0[4], y1[4];
         const bool ranks_in = 16 * k + 8 * t < p.rank;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (ranks_in) load_b(v, b_base + min(16 * (i >> 1) + 2 * (i & 1) + n_id, most) * p.rank + 16 * k);
-          y[0][i] = make_uint2(v.x, v.y);
-          y[1][i] = make_uint2(v.z, v.w);
+          if (ranks_in) load_b(v, id0 + min(16 * (i >> 1) + 2 * (i & 1), most) * p.rank + 16 * k);
+          y0[i] = make_uint2(v.x, v.y);
+          y1[i] = make_uint2(v.z, v.w);
         }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint4* a_at = u + (k + q) * kTerms * 32;
-          const uint4 a[kTerms] = {a_at[0], a_at[32], a_at[64]};
-          step_products(d, a, y[q]);
-        }
+        const uint4* a_at = u + k * kTerms * 32;
+        const uint4 a0[kTerms] = {a_at[0], a_at[32], a_at[64]};
+        const uint4 a1[kTerms] = {a_at[96], a_at[128], a_at[160]};
+        step_products<false>(d, a0, y0);
+        step_products<false>(d, a1, y1);
       }
       add_sums(x, d);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j = jh + 16 * b + 4 * t;
-        if (r[i] >= 0 && j < p.V_s)
-          *reinterpret_cast<float4*>(p.out[slice] + row_at[i] + j) = x[i][b];
-        else
-          x[i][b] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      }
+    store_quarter(p.out[slice], row_at, r, j, p.V_s, t, x);
     if (p.stats != nullptr) {
-      const HalfStats now[2] = {half_stats(x[0]), half_stats(x[1])};
-      if (h & 1) {
-        const int block = w.block0 + (h >> 1);
+      quarter_stats(stats[0], h & 3, x[0]);
+      quarter_stats(stats[1], h & 3, x[1]);
+      if ((h & 3) == 3) {
+        const int block = w.block0 + (h >> 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (r[i] >= 0 && t == 0)
-            write_stats(stats[i], now[i], p.stats + (static_cast<size_t>(r[i]) * p.S * p.B + block) * 8);
+          write_stats(stats[i], p.stats + (static_cast<size_t>(max(r[i], 0)) * p.S * p.B + block) * 8,
+                      r[i] >= 0 && t == 0);
       }
-      stats[0] = now[0];
-      stats[1] = now[1];
     }
-    if ((h & 1) && ++in_slice == p.B) {
+    if ((h & 3) == 3 && ++in_slice == p.B) {
       in_slice = 0;
       ++slice;
     }

@@ -17,8 +17,8 @@
 // [2^-40, 2^60] (a NaN or +inf logit; none above -inf; logits some 30 T above
 // the first ones read, or all of them some 28 T below 0) or whose k exceeds
 // 2^20 is done again in the careful form.  c's rounding is a temperature off by at
-// most 2^-24, used consistently: log p_t moves by 2^-24 of its size at most,
-// and with w at hand the first-order term is taken out.
+// most 2^-24, used consistently: log p_t moves by at most 2^-24 of its distance
+// from the mean of x.
 //
 // The careful form keeps each thread's running maximum, e_j = exp((l_j - m) /
 // T) with c as a sum of two floats, and rescales when the maximum grows.
@@ -252,10 +252,7 @@ __device__ __forceinline__ RowScore row_score(const PartStats& s, float token_lo
   r.logprob = x - r.log_z;
   r.entropy = 0.0;
   if (ENT) {
-    const double mean = s.w * kExpMean / r.z;  // of x under p
-    r.entropy = r.log_z - mean;
-    // the temperature that c has, to first order
-    if (FAST && x > -1e30) r.logprob += (c.inv_t / c.inv_t_fast - 1.0) * (x - mean);
+    r.entropy = r.log_z - s.w * kExpMean / r.z;  // less the mean of x under p
     if (r.entropy < 0.0) r.entropy = 0.0;
   }
   if (r.logprob > 0.0) r.logprob = 0.0;
