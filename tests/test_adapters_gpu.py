@@ -47,6 +47,9 @@ def _check(out, logits, hidden, a, b, ids, scale):
     (130, 128, 2, 516, 5, 48),
     (20, 64, 2, 144, 3, 256),      # the largest rank
     (1000, 64, 1, 64, 7, 16),      # many rows, few ids
+    (600, 64, 16, 132, 9, 32),     # three tiles of rows, blocks over many slices
+    (300, 1040, 2, 1000, 40, 64),  # H shared by a cluster, ragged units
+    (280, 72, 3, 20, 4, 56),       # slices of less than a block
 ])
 def test_parity(cuda_device, R, H, S, V_s, n, rank):
     hidden, logits, a, b, scale, ids = _inputs(R, H, S, V_s, n, rank, R + rank, cuda_device)
@@ -65,6 +68,42 @@ def test_parity(cuda_device, R, H, S, V_s, n, rank):
     over = [x.clone() for x in logits]
     vsl.adapters_add(over, hidden, a, b, ids, scale=scale, out=over)
     assert all(torch.equal(x, y) for x, y in zip(over, want))
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 64, 72, 128, 200, 256])
+@pytest.mark.parametrize("per", [1, 2, 3])
+def test_units_of_few_rows(cuda_device, rank, per):
+    """Every adapter with one, two or three rows: multiply-adds up to two, products above."""
+    R = 6 * per
+    ids = np.arange(R) // per
+    hidden, logits, a, b, scale, ids = _inputs(R, 72, 2, 300, 6, rank, rank + per, cuda_device, ids)
+    out, stats = vsl.adapters_add(logits, hidden, a, b, ids, scale=scale, tile_stats=True)
+    _check(out, logits, hidden, a, b, ids, scale)
+    ref = vsl.tile_stats(out)
+    assert torch.equal(stats[..., :4], ref[..., :4]) and torch.equal(stats[..., 5:], ref[..., 5:])
+    assert bool(((stats[..., 4] - ref[..., 4]).abs() <= ref[..., 4] * 2 * (2.0 ** -22 + 2.0 ** -19 + 2.0 ** -17)).all())
+
+
+@pytest.mark.parametrize("pattern", ["alone", "three"])
+def test_statistics_of_unusual_logits(cuda_device, pattern):
+    """-inf, +inf, NaN and zeros in the base logits: the records are those of the statistics kernel on the result."""
+    R = 8
+    ids = {"alone": np.arange(R), "three": np.arange(R) // 3}[pattern]
+    hidden, logits, a, b, scale, ids = _inputs(R, 64, 2, 388, 8, 16, 6, cuda_device, ids)
+    a[0], b[0][1], b[1][1] = 0.0, 0.0, 0.0
+    for x in logits:
+        x[0, 3:40], x[1, 128:256], x[2, 7], x[3, 200], x[4, 384:] = 0.0, -np.inf, np.inf, np.nan, -np.inf
+        x[5] = -np.inf
+    out, stats = vsl.adapters_add(logits, hidden, a, b, ids, scale=scale, tile_stats=True)
+    ref = vsl.tile_stats(out)
+    quarter_nan = torch.cat([torch.nn.functional.pad(x, (0, -388 % 128)).view(R, -1, 4, 32).isnan().any(3) for x in out], 1)
+    same = (stats[..., :4] == ref[..., :4]) | quarter_nan         # a quarter that holds a NaN has no maximum to agree on
+    assert bool(same.all())
+    assert torch.equal(stats[..., 5:], ref[..., 5:])
+    s, r = stats[..., 4], ref[..., 4]
+    bad = ~torch.isfinite(r)
+    assert torch.equal(bad, ~torch.isfinite(s)) and torch.equal(r.isnan(), s.isnan())
+    assert bool(((s - r).abs() <= r * 2 * (2.0 ** -22 + 2.0 ** -19 + 2.0 ** -17))[~bad].all())
 
 
 @pytest.mark.parametrize("pattern", ["one", "none", "runs", "distinct", "alternate"])

@@ -13,7 +13,8 @@ FMIN = float(np.finfo(np.float32).min)
 
 # rows, slices, ids per slice: one id group to several slices, odd sizes, more rows than CTAs, a long row
 SHAPES = [(1, 1, 4), (3, 1, 8), (5, 3, 20), (4, 2, 512), (7, 16, 4), (33, 5, 1004), (300, 1, 260), (2, 4, 37984),
-          (3, 1, 151936), (1, 8, 32768)]
+          (3, 1, 151936), (1, 8, 32768),
+          (1500, 3, 100), (500, 2, 6000), (160, 1, 12000), (40, 4, 20000)]   # one to eight CTAs per row, several rows each
 
 
 def _rng(*k):
@@ -58,39 +59,87 @@ def _close(got, want, bound, what):
         f"{got[bad][0]} against {want[bad][0]} (bound {np.broadcast_to(bound, got.shape)[bad][0]})"
 
 
-@pytest.mark.parametrize("T", [1.0, 0.37])
-@pytest.mark.parametrize("R,S,V_s", SHAPES)
-def test_logprobs_and_gradient(cuda_device, R, S, V_s, T):
-    rng = _rng(R, S, V_s)
-    l = _logits(R, S * V_s, rng)
-    tokens = _tokens(l, rng)
-    slices = _slices(l, S, cuda_device)
-    tok = _dev(tokens, cuda_device, torch.int32)
+def _check_logprobs(l, tokens, S, T, rng, dev):
+    R, V = l.shape
+    V_s, T64 = V // S, np.float64(np.float32(T))
+    slices = _slices(l, S, dev)
+    tok = _dev(tokens, dev, torch.int32)
     fwd = vsl.token_logprobs(slices, tok, temperature=T, entropy=True)
-    lp, ent = O.token_logprobs(l, tokens, T)
-    logp = O.log_softmax(l, np.float64(np.float32(T)))
-    lp, ent = O.token_logprobs(l, tokens, np.float64(np.float32(T)))
+    logp = O.log_softmax(l, T64)
+    lp, ent = O.token_logprobs(l, tokens, T64)
     _close(fwd.logprob, lp, B.logprob_bound(logp, lp), "logprob")
     _close(fwd.entropy, ent, B.entropy_bound(logp, ent), "entropy")
     alone = vsl.token_logprobs(slices, tok, temperature=T)
     assert alone.entropy is None and torch.equal(alone.row_stats, fwd.row_stats)
+    assert torch.equal(alone.logprob, fwd.logprob)
     dl, de = rng.normal(size=R).astype(np.float32), rng.normal(size=R).astype(np.float32)
     dl[R // 2] = 0.0
-    on = O.counts(tokens, S * V_s)
+    on = O.counts(tokens, V)
     for d_ent in (None, de):
-        want = O.token_logprobs_grad(l, tokens, dl, d_ent, np.float64(np.float32(T)))
+        want = O.token_logprobs_grad(l, tokens, dl, d_ent, T64)
         h = np.where(on, 0.0 if d_ent is None else d_ent, 0.0)
         for kind, dtype in (("fp32", torch.float32), ("bf16", torch.bfloat16)):
-            got = vsl.token_logprobs_grad(slices, tok, fwd, _dev(dl, cuda_device), _dev(d_ent, cuda_device),
-                                          grad_dtype=dtype)
+            got = vsl.token_logprobs_grad(slices, tok, fwd, _dev(dl, dev), _dev(d_ent, dev), grad_dtype=dtype)
             assert all(x.dtype == dtype and x.shape == (R, V_s) for x in got)
             zero = np.zeros(R)
             bound = B.grad_bound(logp, tokens, T, np.where(on, dl, 0.0), h, zero, zero, want, kind)
             _close(_cat(got), want, bound, f"gradient {kind}")
     in_place = [x.clone() for x in slices]
-    first = vsl.token_logprobs_grad(slices, tok, fwd, _dev(dl, cuda_device), _dev(de, cuda_device))
-    vsl.token_logprobs_grad(in_place, tok, fwd, _dev(dl, cuda_device), _dev(de, cuda_device), grad=in_place)
+    first = vsl.token_logprobs_grad(slices, tok, fwd, _dev(dl, dev), _dev(de, dev))
+    vsl.token_logprobs_grad(in_place, tok, fwd, _dev(dl, dev), _dev(de, dev), grad=in_place)
     assert all(torch.equal(x, y) for x, y in zip(first, in_place))
+
+
+@pytest.mark.parametrize("T", [1.0, 0.37])
+@pytest.mark.parametrize("R,S,V_s", SHAPES)
+def test_logprobs_and_gradient(cuda_device, R, S, V_s, T):
+    rng = _rng(R, S, V_s)
+    l = _logits(R, S * V_s, rng)
+    _check_logprobs(l, _tokens(l, rng), S, T, rng, cuda_device)
+
+
+def _extreme_rows(V, rng):
+    """Rows whose logits are far from what a row begins with, from 0 or from one another."""
+    l = rng.normal(size=(12, V)).astype(np.float32)
+    l[1] += 5e6
+    l[2, : V // 2] = -1e4                            # a mask of a large finite value, first
+    l[3, -1] = 200.0                                 # far above all that came before
+    l[4] = FMIN                                      # nothing but the lowest value
+    l[5, : V // 3] = FMIN
+    l[6] *= np.float32(1e30)
+    l[7] -= 300.0
+    l[8] = -1e9
+    l[8, [5, V // 2, V - 1]] = [1.0, 2.0, 3.0]
+    l[9] = -np.inf
+    l[9, V - 2] = -70.0                              # one finite logit
+    l[10, : V - 4] = -np.inf
+    l[11] = 3e38
+    l[11, 7] = -3e38
+    return l
+
+
+def _extreme_tokens(l):
+    return np.array([int(np.argmax(x)) if i % 2 else int(np.flatnonzero(np.isfinite(x))[0]) for i, x in enumerate(l)], np.int32)
+
+
+@pytest.mark.parametrize("V,S,T", [(8, 1, 1.0), (2000, 2, 1.0), (20000, 2, 1.0), (20000, 1, 0.5), (151936, 4, 1.0),
+                                   (2000, 2, 1e-6), (2000, 2, 1e6)])
+def test_extreme_rows(cuda_device, V, S, T):
+    rng = _rng(V, S, 3)
+    l = _extreme_rows(V, rng)
+    tokens = _extreme_tokens(l)
+    T64 = np.float64(np.float32(T))
+    lp, _ = O.token_logprobs(l, tokens, T64)
+    keep = np.abs(lp) < 1e30                         # a token at -1e35 of the rest has no ratio to speak of
+    tokens[~keep] = -1
+    _check_logprobs(l, tokens, S, T, rng, cuda_device)
+    lp, _ = O.token_logprobs(l, tokens, T64)
+    old = np.asarray(lp - 0.05, np.float32)
+    far = np.abs(lp) > 1e3                           # float32 old logprobs cannot name a ratio near 1 there
+    tokens[far] = -1
+    adv, w = rng.normal(size=12).astype(np.float32), np.ones(12, np.float32)
+    _check_policy(l, tokens, S, T, old, old.copy(), adv, w, 0.0, 0.0, cuda_device)
+    _check_policy(l, tokens, S, T, old, old.copy(), adv, w, 0.1, 0.03, cuda_device)
 
 
 def _policy_case(R, V, rng, l, tokens, T):
@@ -106,24 +155,19 @@ def _policy_case(R, V, rng, l, tokens, T):
     return old, ref, adv, w
 
 
-@pytest.mark.parametrize("kl_coef,ent_coef,T", [(0.0, 0.0, 1.0), (0.05, 0.0, 0.8), (0.1, 0.03, 1.3)])
-@pytest.mark.parametrize("R,S,V_s", SHAPES)
-def test_policy_loss(cuda_device, R, S, V_s, kl_coef, ent_coef, T):
-    rng = _rng(R, S, V_s, 1)
-    T64, V = np.float64(np.float32(T)), S * V_s
-    l = _logits(R, V, rng)
-    tokens = _tokens(l, rng)
-    old, ref, adv, w = _policy_case(R, V, rng, l, tokens, T64)
+def _check_policy(l, tokens, S, T, old, ref, adv, w, kl_coef, ent_coef, dev):
+    R, V = l.shape
+    T64 = np.float64(np.float32(T))
     f64 = lambda x: np.float64(np.float32(x))  # noqa: E731
     want = O.policy_loss(l, tokens, old, adv, T=T64, weights=w, ref=ref, lo=f64(0.2), hi=f64(0.28), kl_coef=f64(kl_coef),
                          ent_coef=f64(ent_coef))
-    slices, tok = _slices(l, S, cuda_device), _dev(tokens, cuda_device, torch.int32)
-    rows = [_dev(x, cuda_device) for x in (old, adv, w, ref)]
+    slices, tok = _slices(l, S, dev), _dev(tokens, dev, torch.int32)
+    rows = [_dev(x, dev) for x in (old, adv, w, ref)]
     kw = dict(weights=rows[2], ref_logprob=rows[3], clip_low=0.2, clip_high=0.28, kl_coef=kl_coef,
               entropy_coef=ent_coef, temperature=T)
     logp = O.log_softmax(l, T64)
     on = O.counts(tokens, V, w)
-    err = np.where(on, B.logprob_bound(logp, 0 * adv), 0.0)         # of the logprob inside the kernel (64 bits after z)
+    err = np.where(on, B.logprob_bound(logp, want["logprob"]), 0.0)   # of the logprob inside the kernel
     err_h = np.where(on, B.entropy_bound(logp, 0 * adv), 0.0)
     ratio = np.where(on, np.exp(want["logprob"] - np.where(on, old, 0)), 0.0)
     d = np.where(on, ref - want["logprob"], 0.0)
@@ -144,6 +188,16 @@ def test_policy_loss(cuda_device, R, S, V_s, kl_coef, ent_coef, T):
     none = vsl.policy_loss(slices, tok, rows[0], rows[1], grad=False, **kw)
     assert none.grad is None and torch.equal(none.loss, plain.loss) and torch.equal(same.loss, plain.loss)
     assert all(torch.equal(x, y) for x, y in zip(plain.grad, over))
+
+
+@pytest.mark.parametrize("kl_coef,ent_coef,T", [(0.0, 0.0, 1.0), (0.05, 0.0, 0.8), (0.1, 0.03, 1.3)])
+@pytest.mark.parametrize("R,S,V_s", SHAPES)
+def test_policy_loss(cuda_device, R, S, V_s, kl_coef, ent_coef, T):
+    rng = _rng(R, S, V_s, 1)
+    l = _logits(R, S * V_s, rng)
+    tokens = _tokens(l, rng)
+    old, ref, adv, w = _policy_case(R, S * V_s, rng, l, tokens, np.float64(np.float32(T)))
+    _check_policy(l, tokens, S, T, old, ref, adv, w, kl_coef, ent_coef, cuda_device)
 
 
 def test_policy_gradient_against_differences(cuda_device):
