@@ -23,7 +23,7 @@
 #include <type_traits>
 
 #include "vsl_internal.h"
-#include "vsl_ptx.cuh"
+#include "vsl_ptx_rows.cuh"
 
 namespace vsl {
 

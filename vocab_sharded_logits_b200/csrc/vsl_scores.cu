@@ -20,7 +20,7 @@
 #include <mutex>
 
 #include "vsl_internal.h"
-#include "vsl_ptx.cuh"
+#include "vsl_ptx_rows.cuh"
 #include "vsl_softmax.cuh"
 
 namespace vsl {
