@@ -67,6 +67,7 @@ typedef enum {
 #define VSL_MAX_LOGPROBS 20     /* 0 <= n_logprobs <= 20 (and <= S * V_s)   */
 #define VSL_MAX_SPEC 64         /* speculative tokens per request in vsl_verify_drafts */
 #define VSL_MAX_RANK 256        /* adapter rank in vsl_adapters_add         */
+#define VSL_MAX_ADAPTER_ROWS (1 << 30) /* R in vsl_adapters_add         */
 #define VSL_MAX_VOCAB (1 << 30) /* S * V_s in the calls that score tokens and in vsl_adapters_add */
 
 /* Type of a gradient written to vocab slices. */
@@ -350,7 +351,7 @@ VSL_API size_t vsl_adapters_workspace_bytes(int32_t R, int32_t n_adapters, int32
  *                   written and read by this call's kernels only.  Calls that
  *                   can run at the same time (two streams, or two captured
  *                   graphs) need a workspace each.
- *   R >= 1, H >= 8 with H % 8 == 0, V_s % 4 == 0, n_adapters >= 1,
+ *   1 <= R <= VSL_MAX_ADAPTER_ROWS, H >= 8 with H % 8 == 0, V_s % 4 == 0, n_adapters >= 1,
  *   8 <= rank <= VSL_MAX_RANK with rank % 8 == 0 (adapters of lower rank are
  *   padded with zeros), S * V_s <= VSL_MAX_VOCAB.
  * Errors: VSL_ERR_INVALID_ARG, VSL_ERR_ALIGNMENT, VSL_ERR_UNSUPPORTED,
@@ -362,8 +363,7 @@ VSL_API vsl_status vsl_adapters_add(const float* const* logits_slices, float* co
                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Logprobs of given tokens, and the losses made of them.  With x_j = l_j / T
- * over the whole row (all slices), p its softmax, m = max_j l_j and
- * z = sum_j exp((l_j - m) / T):
+ * over the whole row (all slices) and p its softmax:
  *   logprob = log p_token,   entropy = -sum_j p_j log p_j.
  * In every call below a row whose token lies outside [0, S * V_s) (-1 by
  * convention: prompt tokens, padding, a row the sampler flagged) does not
@@ -378,8 +378,10 @@ VSL_API vsl_status vsl_adapters_add(const float* const* logits_slices, float* co
  *   logprob   : device fp32 [R]       (output)
  *   entropy   : device fp32 [R]       (output, may be NULL)
  *   row_stats : device fp32 [R][2], 8-byte aligned (output, may be NULL):
- *               (m, z), what vsl_token_logprobs_grad takes; (0, 1) for a row
- *               that does not count.
+ *               what vsl_token_logprobs_grad takes: the row's sum of
+ *               exponentials and what they are relative to, in a form of the
+ *               library's own (not for other uses); (0, 1) for a row that does
+ *               not count.
  * Errors: VSL_ERR_INVALID_ARG, VSL_ERR_ALIGNMENT, VSL_ERR_UNSUPPORTED,
  *         VSL_ERR_CUDA. */
 VSL_API vsl_status vsl_token_logprobs(const float* const* logits_slices, int32_t R, int32_t S, int32_t V_s,

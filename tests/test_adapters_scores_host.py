@@ -155,3 +155,8 @@ def test_binding_checks_tensors_before_the_library():
     fwd = v.TokenLogprobs(f, None, torch.zeros(4, 2), 1.0)
     with pytest.raises(ValueError, match="entropy"):
         v.token_logprobs_grad(x, ids, fwd, f, d_entropy=f)
+
+
+def test_adapters_refuse_rows_that_overflow_their_plan():
+    assert v.adapters_workspace_bytes((1 << 30) + 1, 2, 8) == 0 and v.adapters_workspace_bytes(1 << 30, 300, 256) > 1 << 40
+    assert _adapters(R=(1 << 30) + 1, V_s=4, ws_bytes=1 << 60) == UNSUPPORTED

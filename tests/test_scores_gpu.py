@@ -360,3 +360,50 @@ def test_graph_capture_and_another_stream(cuda_device):
     torch.cuda.synchronize()
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("smoothing", [0.0, 1.0])
+def test_a_term_without_weight_may_be_infinite(cuda_device, smoothing):
+    """A token of probability 0 makes one of the two terms infinite; left out, it does not matter."""
+    at = torch.tensor([0, 1, 2], dtype=torch.int32, device=cuda_device)
+    lp = torch.tensor([-np.inf, -1.0] if smoothing else [-1.0, -np.inf], device=cuda_device)
+    got = vsl.preference_loss(lp, None, at, 0.5, smoothing)
+    assert got.loss.item() == 0.0 and bool((got.d_logprob == 0).all())
+
+
+def test_an_output_filled_again_holds_no_older_entropy(cuda_device):
+    rng = _rng(21)
+    old, new = (_slices(_logits(5, 2000, rng), 2, cuda_device) for _ in range(2))
+    tok = _dev(_tokens(_logits(5, 2000, rng, masked=False), rng), cuda_device, torch.int32)
+    out = vsl.token_logprobs(old, tok, entropy=True)
+    before = out.entropy.clone()
+    assert vsl.token_logprobs(new, tok, out=out) is out and not torch.equal(out.entropy, before)
+    assert torch.equal(out.entropy, vsl.token_logprobs(new, tok, entropy=True).entropy)
+
+
+def test_two_streams_at_once(cuda_device):
+    """Losses of different batches overlapping on two streams, again and again: each as when run alone."""
+    rng = _rng(22)
+    sizes = [(150, 2, 20000), (40, 4, 37984)]
+    batches = []
+    for R, S, V_s in sizes:
+        l = _logits(R, S * V_s, rng)
+        batches.append((_slices(l, S, cuda_device), _dev(_tokens(l, rng), cuda_device, torch.int32),
+                        torch.ones(R, device=cuda_device)))
+
+    def step(batch, stream=None):
+        s, tok, one = batch
+        p = vsl.policy_loss(s, tok, -9 * one, one, entropy_coef=0.01, stream=stream)
+        f = vsl.token_logprobs(s, tok, entropy=True, stream=stream)
+        g = vsl.token_logprobs_grad(s, tok, f, one, one, stream=stream)
+        return [p.loss, *p.grad, f.logprob, f.entropy, *g]
+    want = [step(b) for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for b, stream in zip(batches, streams):
+            with torch.cuda.stream(stream):
+                got.append(step(b))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for w, g in zip(want, got) for x, y in zip(w, g))

@@ -413,7 +413,7 @@ def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, ou
 
 class TokenLogprobs:
     """Outputs of ``token_logprobs``: logprob [R], entropy [R] (when asked for), row_stats [R, 2]
-    (the row's largest logit m and sum of exp((l - m) / T)) and the temperature they hold for."""
+    (what ``token_logprobs_grad`` takes, in the library's own form) and the temperature they hold for."""
 
     def __init__(self, logprob, entropy, row_stats, temperature):
         self.logprob = logprob
@@ -427,14 +427,15 @@ def token_logprobs(logits_slices, token_ids, temperature=1.0, entropy=False, out
     the row's entropy.
 
     logits_slices: list of fp32 [R, V_s] CUDA tensors; token_ids: int32 [R] (outside the vocabulary,
-    -1 by convention: the row does not count, its outputs are 0).
+    -1 by convention: the row does not count, its outputs are 0).  out: a ``TokenLogprobs`` to fill
+    again (its entropy too, where it holds one).
     """
     if out is None:
         return TokenLogprobs(*_binding.token_logprobs(logits_slices, token_ids, temperature, entropy, None, None, None,
                                                       _handle(stream)), float(temperature))
     if entropy and out.entropy is None:
         raise ValueError("out.entropy is missing")
-    _binding.token_logprobs(logits_slices, token_ids, temperature, entropy, out.logprob, out.entropy, out.row_stats,
+    _binding.token_logprobs(logits_slices, token_ids, temperature, out.entropy is not None, out.logprob, out.entropy, out.row_stats,
                             _handle(stream))
     out.temperature = float(temperature)
     return out

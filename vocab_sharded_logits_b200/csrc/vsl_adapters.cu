@@ -922,12 +922,13 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   // up to 64 ranks to a CTA; the CTAs of a cluster share longer rows of H while
   // the units are few
   const int steps = rank_steps(rank);
-  const int groups = steps < 4 ? steps : 4, ctas = z.tiles * z.slots * ((steps + groups - 1) / groups);
+  const int groups = steps < 4 ? steps : 4, rank_parts = (steps + groups - 1) / groups;
+  const long long ctas = static_cast<long long>(z.tiles) * z.slots * rank_parts;
   sa.split = H < 4 * 256 || ctas > 296 ? 1 : ctas > 148 ? 2 : kMaxSplit;
   {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
-    cfg.gridDim = dim3(z.tiles, z.slots, (steps + groups - 1) / groups * sa.split);
+    cfg.gridDim = dim3(z.tiles, z.slots, rank_parts * sa.split);
     cfg.blockDim = dim3(kShrinkWarps * 32);
     cfg.stream = stream;
     attr.id = cudaLaunchAttributeClusterDimension;

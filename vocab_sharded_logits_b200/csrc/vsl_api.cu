@@ -199,7 +199,8 @@ vsl_status vsl_verify_drafts(const int32_t* token_ids, const float* token_logpro
 }
 
 size_t vsl_adapters_workspace_bytes(int32_t R, int32_t n_adapters, int32_t rank) {
-  if (R <= 0 || n_adapters <= 0 || rank <= 0 || rank > VSL_MAX_RANK) return 0;
+  if (R <= 0 || n_adapters <= 0 || rank <= 0 || rank > VSL_MAX_RANK || R > VSL_MAX_ADAPTER_ROWS)
+    return 0;
   return vsl::adapters_workspace_bytes(R, n_adapters, rank);
 }
 
@@ -214,7 +215,7 @@ vsl_status vsl_adapters_add(const float* const* logits_slices, float* const* out
   if (H <= 0 || n_adapters <= 0 || rank <= 0) return VSL_ERR_INVALID_ARG;
   vsl_status st = vsl::check_slices(logits_slices, R, S, V_s);
   if (st != VSL_OK) return st;
-  if (rank > VSL_MAX_RANK) return VSL_ERR_UNSUPPORTED;
+  if (rank > VSL_MAX_RANK || R > VSL_MAX_ADAPTER_ROWS) return VSL_ERR_UNSUPPORTED;
   if (H % 8 != 0 || rank % 8 != 0) return VSL_ERR_ALIGNMENT;
   if (!vsl::aligned16(hidden_bf16) || !vsl::aligned16(a_bf16)) return VSL_ERR_ALIGNMENT;
   for (int s = 0; s < S; ++s) {

@@ -79,7 +79,9 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const __grid_c
       s[i] = a.beta * block_sum(v, shared);
     }
     const double h = s[0] - s[1];
-    loss = w * (-(1.0 - a.smoothing) * log_sigmoid(h) - (a.smoothing != 0.0 ? a.smoothing * log_sigmoid(-h) : 0.0));
+    // a factor of 0 leaves its term out, an infinite one too
+    loss = w * -((a.smoothing != 1.0 ? (1.0 - a.smoothing) * log_sigmoid(h) : 0.0) +
+                 (a.smoothing != 0.0 ? a.smoothing * log_sigmoid(-h) : 0.0));
     d = w * a.beta * (a.smoothing * sigmoid(h) - (1.0 - a.smoothing) * sigmoid(-h));
   }
   if (threadIdx.x == 0) {
