@@ -9,6 +9,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -168,10 +169,10 @@ struct OutSlices {
     list = PyList_New(in.S);
     if (list == nullptr) throw Raised();
     const bool one = static_cast<int64_t>(in.R) * in.V_s % 8 == 0;
-    at::Tensor all;
-    if (one) all = empty({in.S, in.R, in.V_s}, type, in.device);
+    std::vector<at::Tensor> parts;
+    if (one) parts = empty({in.S, in.R, in.V_s}, type, in.device).unbind(0);
     for (int s = 0; s < in.S; ++s) {
-      const at::Tensor t = one ? all.select(0, s) : empty({in.R, in.V_s}, type, in.device);
+      const at::Tensor t = one ? std::move(parts[s]) : empty({in.R, in.V_s}, type, in.device);
       at.push_back(t.data_ptr());
       PyList_SET_ITEM(list, s, wrap(t));
     }
@@ -309,7 +310,8 @@ PyObject* policy_loss(PyObject* const* a, Py_ssize_t n) {
     Py_INCREF(grad_list);
   }
   PyTuple_SET_ITEM(result, 4, grad_list);
-  for (int k = 0; k < 4; ++k) PyTuple_SET_ITEM(result, k, wrap(rows.select(0, k)));
+  const std::vector<at::Tensor> outputs = rows.unbind(0);
+  for (int k = 0; k < 4; ++k) PyTuple_SET_ITEM(result, k, wrap(outputs[k]));
   return result;
 }
 
@@ -402,6 +404,9 @@ PyObject* adapters_add(PyObject* const* a, Py_ssize_t n) {
 // No C++ exception leaves an entry point.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  // outputs and their views are made without the bookkeeping of gradients (a
+  // microsecond of a small call)
+  const at::AutoDispatchBelowADInplaceOrView no_grad;
   try {
     return F(args, n);
   } catch (const Raised&) {
