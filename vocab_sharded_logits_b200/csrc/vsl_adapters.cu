@@ -36,11 +36,17 @@ constexpr int kExpandWarps = 4;
 constexpr int kTerms = 3;         // bf16 terms of u
 constexpr int kFragment = 32 * 4; // 32-bit registers of one A operand (16 x 16 bf16) over a warp
 constexpr int kMaxSplit = 4;      // CTAs that share H
-constexpr int kFewRows = 2;       // a unit of so few rows is done with float32 multiply-adds
+constexpr int kFewRows = 2;       // see few_rows_of
 
 // Products of 16 ranks: one, or an even number (a lane then loads 8 ranks of B
 // at a time, which serve two).
 __host__ __device__ constexpr int rank_steps(int rank) { return rank <= 16 ? 1 : (rank + 31) / 32 * 2; }
+// Units of at most so many rows are done with float32 multiply-adds: of 16 rows
+// of a product 14 or more would be empty, and u is as long as a lane's own share
+// of it.  64 rows of as many adapters of rank 16: 78 us, 111 by products; 32
+// adapters of two rows 54, 68; at rank 32 127 and 138, 80 and 82; at rank 64
+// it is the products that are faster, 234 us (284) and 130 (168).
+__host__ __device__ constexpr int few_rows_of(int rank) { return rank <= 32 ? kFewRows : 0; }
 // Units a tile of `rows` rows over n adapters can have: full ones, a ragged one
 // per adapter and one of rows without an adapter.
 __host__ __device__ constexpr int unit_slots(int rows, int n) {
@@ -86,16 +92,15 @@ struct ShrinkArgs {
   int R, H, n, rank, slots, split;
 };
 
-// CTA (tile, unit, up to 16 GROUPS ranks x a part of H): the warps split the
+// CTA (tile, unit, 16 ranks x a part of H): the warps split the
 // part, the CTAs of a cluster share H.
-template <int GROUPS>
 __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(const __grid_constant__ ShrinkArgs p) {
   __shared__ int key[kTile];
   __shared__ int order[kTile];        // sorted position -> row of the tile
   __shared__ int within[kTile];       // sorted position -> rows of its adapter before it
   __shared__ int starts[kTile + 1];   // unit -> its first sorted position
   __shared__ int warp_units[kShrinkWarps];
-  constexpr int kRanks = 16 * GROUPS;
+  constexpr int kRanks = 16;
   __shared__ float part[kShrinkWarps / 2][kUnitRows][kRanks];
   __shared__ float parts[kMaxSplit][kUnitRows][kRanks];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -162,26 +167,26 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
   for (int i = 0; i < 2; ++i)
     h_row[i] = p.hidden + static_cast<size_t>(row0 + order[first + (row_ok[i] ? g + 8 * i : 0)]) * p.H;
   const __nv_bfloat16* a_row = p.a + (static_cast<size_t>(adapter) * p.rank + k0 + g) * p.H;
-  float d[2 * GROUPS][4] = {};
+  float d[2][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // 32 columns of H a step: a lane's 8 consecutive ones serve two products
   // (the order of the summed index is free, the same on both sides).  The
   // loop's bound is the warp's, not the lane's: every lane takes part in a
   // product, with zeros past the end of H.
-#pragma unroll (GROUPS > 2 ? 2 : 4)
+#pragma unroll 4
   for (int h0 = (split_rank * kShrinkWarps + warp) * 32; h0 < p.H; h0 += p.split * kShrinkWarps * 32) {
     const int h = h0 + 8 * t;
     const bool in = h < p.H;
-    uint4 x[2], y[2 * GROUPS];
+    uint4 x[2], y[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) x[i] = in && row_ok[i] ? __ldg(reinterpret_cast<const uint4*>(h_row[i] + h)) : zero;
 #pragma unroll
-    for (int i = 0; i < 2 * GROUPS; ++i)
+    for (int i = 0; i < 2; ++i)
       y[i] = in && k0 + 8 * i + g < p.rank
                  ? __ldg(reinterpret_cast<const uint4*>(a_row + static_cast<size_t>(8 * i) * p.H + h))
                  : zero;
 #pragma unroll
-    for (int i = 0; i < 2 * GROUPS; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mma_16816(d[i], x[0].x, x[1].x, x[0].y, x[1].y, y[i].x, y[i].y);
       mma_16816(d[i], x[0].z, x[1].z, x[0].w, x[1].w, y[i].z, y[i].w);
     }
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
   for (int round = 0; round < 2; ++round) {
     if (warp / (kShrinkWarps / 2) == 1 - round) {
 #pragma unroll
-      for (int i = 0; i < 2 * GROUPS; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float& to = mine_part[(g + 8 * (q >> 1)) * kRanks + 8 * i + 2 * t + (q & 1)];
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
     float u = (&parts[0][0][0])[e];
     for (int c = 1; c < p.split; ++c) u += (&parts[c][0][0])[e];
     if (p.scale != nullptr) u *= p.scale[adapter];
-    if (count <= kFewRows) {  // kept as it is, [row][padded rank]
+    if (count <= few_rows_of(p.rank)) {  // kept as it is, [row][padded rank]
       if (r < count) reinterpret_cast<float*>(unit_u)[r * steps * 16 + rank] = u;
       continue;
     }
@@ -383,18 +388,18 @@ __device__ __forceinline__ float dot8(const uint4& b, const float (&u)[8], float
   return sum;
 }
 
-// Up to ROWS rows of a unit of at most kFewRows over blocks of 128 ids: 15 of 16 rows of a
-// tensor-core product would be empty, and what counts is that B, which no other
-// row shares, streams in.  LANES lanes hold an id's row of B, 8 ranks each: a
-// quarter (32 ids) is LANES loads of 512 contiguous bytes.  The lanes' sums are
-// added and dealt out in one butterfly, after which every lane holds one id of
-// the quarter: LANES' lane `sub` of the ids' group `at` id (32 / LANES) sub + at.
-template <int LANES, int ROWS>
+// The rows of a unit of at most kFewRows over blocks of 128 ids: what counts is
+// that B, which no other row shares, streams in.  LANES lanes hold an id's row
+// of B, 8 ranks each: a quarter (32 ids) is LANES loads of 512 contiguous bytes.
+// The lanes' sums are added and dealt out in one butterfly, after which every
+// lane holds one id of the quarter: LANES' lane `sub` of the ids' group `at` id
+// (32 / LANES) sub + at.
+template <int LANES>
 __device__ __forceinline__ void few_rows(const ExpandArgs& p, int adapter, const int32_t* rows, int count, const float* u_rows,
                                          int padded, int block0, int last_block, int lane) {
-  constexpr int kPer = 32 / LANES;              // ids of one load
-  constexpr int kLoads = LANES < 8 ? LANES : 8; // loads of a quarter in flight
-  constexpr int kQuarters = LANES < 8 ? (LANES < 2 ? 4 : 8 / LANES) : 1;  // quarters in flight
+  constexpr int ROWS = kFewRows;
+  constexpr int kPer = 32 / LANES;                      // ids of one load
+  constexpr int kQuarters = LANES < 2 ? 4 : 8 / LANES;  // quarters in flight, LANES loads each
   const int sub = lane % LANES, at = lane / LANES;
   const bool ranks_in = 8 * sub < p.rank;
   float u[ROWS][8];
@@ -427,26 +432,23 @@ __device__ __forceinline__ void few_rows(const ExpandArgs& p, int adapter, const
 #pragma unroll
     for (int m0 = 0; m0 < 4; m0 += kQuarters) {
       float part[ROWS][kQuarters][LANES];
+      uint4 y[kQuarters][LANES];
 #pragma unroll
-      for (int i0 = 0; i0 < LANES; i0 += kLoads) {
-        uint4 y[kQuarters][kLoads];
+      for (int q = 0; q < kQuarters; ++q)
 #pragma unroll
-        for (int q = 0; q < kQuarters; ++q)
+        for (int i = 0; i < LANES; ++i) {
+          y[q][i] = make_uint4(0, 0, 0, 0);
+          // ids past the slice's end read its last one's row instead (their sums are not kept)
+          if (ranks_in) load_b(y[q][i], b + min(32 * (m0 + q) + kPer * i + at, most) * p.rank);
+        }
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i) {
-            y[q][i] = make_uint4(0, 0, 0, 0);
-            // ids past the slice's end read its last one's row instead (their sums are not kept)
-            if (ranks_in) load_b(y[q][i], b + min(32 * (m0 + q) + kPer * (i0 + i) + at, most) * p.rank);
-          }
+      for (int q = 0; q < kQuarters; ++q)
 #pragma unroll
-        for (int q = 0; q < kQuarters; ++q)
+        for (int i = 0; i < LANES; ++i) {
+          part[0][q][i] = dot8(y[q][i], u[0], 0.0f);
 #pragma unroll
-          for (int i = 0; i < kLoads; ++i) {
-            part[0][q][i0 + i] = dot8(y[q][i], u[0], 0.0f);
-#pragma unroll
-            for (int c = 1; c < ROWS; ++c) part[c][q][i0 + i] = count > c ? dot8(y[q][i], u[c], 0.0f) : 0.0f;
-          }
-      }
+          for (int c = 1; c < ROWS; ++c) part[c][q][i] = count > c ? dot8(y[q][i], u[c], 0.0f) : 0.0f;
+        }
 #pragma unroll
       for (int c = 0; c < ROWS; ++c)
         if (c < count) {  // the warp's: a butterfly takes all its lanes
@@ -595,7 +597,7 @@ __device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)
 // The products' N index is laid over the ids so that a lane's sums are 4
 // consecutive ids of a row: column n of the i-th product of 4 is id
 // 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.
-template <int STEPS, int LANES>  // rank_steps, lanes of 8 ranks in few_rows
+template <int STEPS, int LANES>  // rank_steps, lanes of 8 ranks in few_rows (0: no unit comes there)
 __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
     adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
   extern __shared__ uint4 expand_stages[];
@@ -604,10 +606,12 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
   const int g = lane >> 2, t = lane & 3;
   const WarpUnit w = warp_unit(p, warp, STEPS);
   if (!w.work) return;
-  if (w.adapter >= 0 && w.count <= kFewRows) {  // the whole warp's
-    few_rows<LANES, kFewRows>(p, w.adapter, w.entry + 4, w.count, reinterpret_cast<const float*>(w.u), STEPS * 16,
-                              w.block0, w.last_block, lane);
-    return;
+  if constexpr (LANES > 0) {
+    if (w.adapter >= 0 && w.count <= kFewRows) {  // the whole warp's
+      few_rows<LANES>(p, w.adapter, w.entry + 4, w.count, reinterpret_cast<const float*>(w.u), STEPS * 16, w.block0,
+                      w.last_block, lane);
+      return;
+    }
   }
   Stage* stages = reinterpret_cast<Stage*>(expand_stages) + warp * kStages;
   const int r[2] = {w.entry[4 + g], w.entry[4 + g + 8]};
@@ -767,19 +771,12 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
 }
 
 // The same for ranks above 64: B and u are loaded as they are used.
-template <int LANES>
 __global__ void __launch_bounds__(kExpandWarps * 32, 4) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int steps = rank_steps(p.rank);
   const WarpUnit w = warp_unit(p, warp, steps);
   if (!w.work) return;
-  if (w.adapter >= 0 && w.count <= kFewRows) {  // the whole warp's; a row at a time, as many as the registers hold
-    for (int c = 0; c < w.count; ++c)
-      few_rows<LANES, 1>(p, w.adapter, w.entry + 4 + c, 1, reinterpret_cast<const float*>(w.u) + c * steps * 16, steps * 16,
-                         w.block0, w.last_block, lane);
-    return;
-  }
   const int r[2] = {w.entry[4 + g], w.entry[4 + g + 8]};
   const size_t row_at[2] = {static_cast<size_t>(max(r[0], 0)) * p.V_s, static_cast<size_t>(max(r[1], 0)) * p.V_s};
   const uint4* u = reinterpret_cast<const uint4*>(w.u) + lane;
@@ -891,7 +888,7 @@ cudaError_t prepare_expand() {
     allow(adapters_expand_kernel<1, 1>, expand_smem<1>());
     allow(adapters_expand_kernel<1, 2>, expand_smem<1>());
     allow(adapters_expand_kernel<2, 4>, expand_smem<2>());
-    allow(adapters_expand_kernel<4, 8>, expand_smem<4>());
+    allow(adapters_expand_kernel<4, 0>, expand_smem<4>());
   });
   return status[dev];
 }
@@ -919,16 +916,16 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   sa.n = n;
   sa.rank = rank;
   sa.slots = z.slots;
-  // up to 64 ranks to a CTA; the CTAs of a cluster share longer rows of H while
-  // the units are few
+  // the CTAs of a cluster share longer rows of H while the units are few (one row
+  // of rank 16 over H = 4,096: 10.4 us, 14.5 by one CTA; 512 rows over 24 adapters
+  // of rank 32: 172 us, 194)
   const int steps = rank_steps(rank);
-  const int groups = steps < 4 ? steps : 4, rank_parts = (steps + groups - 1) / groups;
-  const long long ctas = static_cast<long long>(z.tiles) * z.slots * rank_parts;
+  const long long ctas = static_cast<long long>(z.tiles) * z.slots * steps;
   sa.split = H < 4 * 256 || ctas > 296 ? 1 : ctas > 148 ? 2 : kMaxSplit;
   {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
-    cfg.gridDim = dim3(z.tiles, z.slots, rank_parts * sa.split);
+    cfg.gridDim = dim3(z.tiles, z.slots, steps * sa.split);
     cfg.blockDim = dim3(kShrinkWarps * 32);
     cfg.stream = stream;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -937,10 +934,7 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
     attr.val.clusterDim.z = sa.split;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    auto kernel = groups == 1   ? adapters_shrink_kernel<1>
-                  : groups == 2 ? adapters_shrink_kernel<2>
-                                : adapters_shrink_kernel<4>;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, sa);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, adapters_shrink_kernel, sa);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -962,19 +956,21 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   ea.slots = z.slots;
   ea.tiles = z.tiles;
   ea.slot_ctas = static_cast<int>((static_cast<long long>(z.tiles) * z.slots + kExpandWarps - 1) / kExpandWarps);
-  // a warp keeps its unit's u over several blocks, while there are warps enough to fill the SMs some times over
+  // A warp keeps its unit's u over several blocks, while there are warps enough
+  // to fill the SMs some times over (64 requests of rank 16: 78 us, 94 with a
+  // block a warp; 2,048 rows over 8 adapters of rank 64: 620 us, 712).  Above
+  // rank 64 it keeps no u (512 rows of rank 256: 545 us, 577 with several blocks).
   ea.warp_blocks = 1;
-  while (ea.warp_blocks < 8 && static_cast<long long>(ea.slot_ctas) * S * ea.B / ea.warp_blocks > 8 * 148 * 4)
+  while (rank <= 64 && ea.warp_blocks < 8 && static_cast<long long>(ea.slot_ctas) * S * ea.B / ea.warp_blocks > 8 * 148 * 4)
     ea.warp_blocks *= 2;
   const long long grid =
       static_cast<long long>(ea.slot_ctas) * ((static_cast<long long>(S) * ea.B + ea.warp_blocks - 1) / ea.warp_blocks);
   if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   const unsigned g = static_cast<unsigned>(grid);
-  if (rank > 128) return launch_after(adapters_expand_wide_kernel<32>, ea, g, 0, stream);
-  if (rank > 64) return launch_after(adapters_expand_wide_kernel<16>, ea, g, 0, stream);
+  if (rank > 64) return launch_after(adapters_expand_wide_kernel, ea, g, 0, stream);
   const cudaError_t e = prepare_expand();
   if (e != cudaSuccess) return e;
-  if (rank > 32) return launch_after(adapters_expand_kernel<4, 8>, ea, g, expand_smem<4>(), stream);
+  if (rank > 32) return launch_after(adapters_expand_kernel<4, 0>, ea, g, expand_smem<4>(), stream);
   if (rank > 16) return launch_after(adapters_expand_kernel<2, 4>, ea, g, expand_smem<2>(), stream);
   if (rank > 8) return launch_after(adapters_expand_kernel<1, 2>, ea, g, expand_smem<1>(), stream);
   return launch_after(adapters_expand_kernel<1, 1>, ea, g, expand_smem<1>(), stream);

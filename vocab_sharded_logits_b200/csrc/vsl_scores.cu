@@ -27,10 +27,8 @@ namespace vsl {
 
 namespace {
 
-constexpr int kThreads = 512;       // of a CTA
-constexpr int kSmallThreads = 128;  // of a CTA of the row kernels where a row has few logits
-constexpr int kSmallUnits = 2048;   // a row of at most so many units is one
-constexpr int kRowThreads = 1536;   // threads of the policy kernel that stand on an SM (40 registers each)
+constexpr int kThreads = 512;       // of a CTA of the gradient kernel
+constexpr int kRowThreads = 1536;   // threads of a row kernel that stand on an SM (40 registers each)
 constexpr int kBatch = 4;      // units of four logits a thread has in flight
 constexpr int kMaxCluster = 8;
 
@@ -597,7 +595,23 @@ cudaError_t device_sms(int* sms) {
   return status[dev];
 }
 
-int row_threads(int units) { return units <= kSmallUnits ? kSmallThreads : kThreads; }
+// Threads of a CTA of the row kernels.  CTAs of 256 finish and make room in
+// smaller steps than of 512 (logprobs of 512 rows of 151,936: 53 us, 64 with
+// 512; of 2,048: 184 us, 201; policy loss of 300 rows of 51,012: 32 us, 35), of
+// 128 only pay on short rows (512 rows of 8,000: 8 us with 128, 10 with 512;
+// 512 rows of 151,936: policy loss 148 us with 128, 133 with 256).  512 where
+// the rows are so few that a CTA each SM's worth would not fill them (policy
+// loss of 16 rows of 262,144: 16.5 us, 18.5 with 256), and in the policy loss
+// where 256 would leave more rows in flight than the L2 cache holds (1,024 rows
+// of 262,144: 424 us, 438).
+constexpr float kL2Room = 96.0f * 1048576.0f;  // of 126 MB
+int row_threads(int R, int units, bool cached, int sms) {
+  if (units <= 2048) return 128;
+  const long long places = static_cast<long long>(kRowThreads) * sms;
+  if (static_cast<long long>(R) * kMaxCluster * 512 <= places) return 512;
+  const float rows = fminf(static_cast<float>(R), static_cast<float>(places / (256 * kMaxCluster)));
+  return cached && rows * units * 16.0f > kL2Room ? 512 : 256;
+}
 
 // CTAs per row (a power of two): the fewest microseconds by a rough count.  The
 // SMs hold kRowThreads threads each, `places` CTAs in all; a full set of CTAs
@@ -609,11 +623,11 @@ int row_threads(int units) { return units <= kSmallUnits ? kSmallThreads : kThre
 // 151,936: 51 us with 4, 45 with 2).  `cached`: the rows being worked on at a
 // time must leave the L2 cache room, at most 96 MB of its 126 (2,048 rows of
 // 151,936: 0.50 ms with 4 CTAs a row, 67 MB; 0.55 with 2, 135 MB).
-cudaError_t choose_cluster(int R, int units, float per_unit, float fixed, bool cached, int* cluster) {
+cudaError_t choose_cluster(int R, int units, float per_unit, float fixed, bool cached, int* cluster, int* threads_out) {
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
   if (e != cudaSuccess) return e;
-  const int threads = row_threads(units);
+  const int threads = *threads_out = row_threads(R, units, cached, sms);
   const float places = static_cast<float>(kRowThreads) * sms / threads;
   float best = 0.0f;
   *cluster = 0;
@@ -621,7 +635,7 @@ cudaError_t choose_cluster(int R, int units, float per_unit, float fixed, bool c
     if (c > 1 && units / c < threads) break;  // a part has a unit or more per thread
     const float sets = static_cast<float>(R) * c / places, whole = floorf(sets), rest = sets - whole;
     const float rows = fminf(static_cast<float>(R), places / c);
-    if (cached && c < kMaxCluster && units / (2 * c) >= threads && rows * units * 16.0f > 96.0f * 1048576.0f) continue;
+    if (cached && c < kMaxCluster && units / (2 * c) >= threads && rows * units * 16.0f > kL2Room) continue;
     const float stream = per_unit * units / (static_cast<float>(c) * threads);
     const float time = whole * (stream + fixed) + (rest > 0.0f ? stream * fmaxf(rest, 0.35f) + fixed : 0.0f);
     if (*cluster == 0 || time < best) {
@@ -632,19 +646,20 @@ cudaError_t choose_cluster(int R, int units, float per_unit, float fixed, bool c
   return static_cast<long long>(R) * *cluster > 0x7FFFFFFFLL ? cudaErrorInvalidConfiguration : cudaSuccess;
 }
 
-cudaError_t row_cluster(int R, int units, int* cluster) { return choose_cluster(R, units, 0.55f, 5.0f, false, cluster); }
+cudaError_t row_cluster(int R, int units, int* cluster, int* threads) {
+  return choose_cluster(R, units, 0.55f, 5.0f, false, cluster, threads);
+}
 
 // keep: the threads hold their parts in registers between the two passes,
 // which pays where all CTAs run at once and time is latency (4 rows of 1,024:
 // 6.3 us, 8.4 without), not where it halves how many do (300 rows of 51,012: 73
 // us, 35 without).
-cudaError_t policy_cluster(int R, int units, int* cluster, bool* keep) {
-  const cudaError_t e = choose_cluster(R, units, 1.1f, 6.0f, true, cluster);
+cudaError_t policy_cluster(int R, int units, int* cluster, int* threads, bool* keep) {
+  const cudaError_t e = choose_cluster(R, units, 1.1f, 6.0f, true, cluster, threads);
   if (e != cudaSuccess) return e;
   int sms = 0;
-  const int threads = row_threads(units);
-  *keep = units <= *cluster * kBatch * threads && device_sms(&sms) == cudaSuccess &&
-          static_cast<long long>(R) * *cluster * threads <= 1024LL * sms;
+  *keep = units <= *cluster * kBatch * *threads && device_sms(&sms) == cudaSuccess &&
+          static_cast<long long>(R) * *cluster * *threads <= 1024LL * sms;
   return cudaSuccess;
 }
 
@@ -672,9 +687,16 @@ cudaError_t launch_policy(const PolicyArgs& a, int R, bool ent, bool keep, cudaS
   return launch_clusters(kernel, a, R, a.cluster, THREADS, stream);
 }
 template <typename T>
-cudaError_t launch_policy(const PolicyArgs& a, int R, bool ent, bool keep, cudaStream_t stream) {
-  return row_threads(a.in.units) == kThreads ? launch_policy<T, kThreads>(a, R, ent, keep, stream)
-                                             : launch_policy<T, kSmallThreads>(a, R, ent, keep, stream);
+cudaError_t launch_policy(const PolicyArgs& a, int R, int threads, bool ent, bool keep, cudaStream_t stream) {
+  return threads == 512   ? launch_policy<T, 512>(a, R, ent, keep, stream)
+         : threads == 256 ? launch_policy<T, 256>(a, R, ent, keep, stream)
+                          : launch_policy<T, 128>(a, R, ent, keep, stream);
+}
+
+template <int THREADS>
+cudaError_t launch_logprobs(const LogprobArgs& a, int R, cudaStream_t stream) {
+  return launch_clusters(a.entropy != nullptr ? token_logprobs_kernel<true, THREADS> : token_logprobs_kernel<false, THREADS>,
+                         a, R, a.cluster, THREADS, stream);
 }
 
 }  // namespace
@@ -688,15 +710,13 @@ cudaError_t launch_token_logprobs(const float* const* logits, int R, int S, int 
   a.logprob = logprob;
   a.entropy = entropy;
   a.stats = reinterpret_cast<float2*>(row_stats);
-  const cudaError_t e = row_cluster(R, a.in.units, &a.cluster);
+  int threads = 0;
+  const cudaError_t e = row_cluster(R, a.in.units, &a.cluster, &threads);
   if (e != cudaSuccess) return e;
   a.per_part = (a.in.units + a.cluster - 1) / a.cluster;
-  const bool ent = entropy != nullptr;
-  if (row_threads(a.in.units) == kThreads)
-    return launch_clusters(ent ? token_logprobs_kernel<true, kThreads> : token_logprobs_kernel<false, kThreads>, a, R,
-                           a.cluster, kThreads, stream);
-  return launch_clusters(ent ? token_logprobs_kernel<true, kSmallThreads> : token_logprobs_kernel<false, kSmallThreads>,
-                         a, R, a.cluster, kSmallThreads, stream);
+  return threads == 512   ? launch_logprobs<512>(a, R, stream)
+         : threads == 256 ? launch_logprobs<256>(a, R, stream)
+                          : launch_logprobs<128>(a, R, stream);
 }
 
 cudaError_t launch_token_logprobs_grad(const float* const* logits, int R, int S, int V_s, const int32_t* token_ids,
@@ -744,12 +764,13 @@ cudaError_t launch_policy_loss(const float* const* logits, int R, int S, int V_s
   a.kl_coef = in.kl_coef;
   a.entropy_coef = in.entropy_coef;
   bool keep = false;
-  const cudaError_t e = policy_cluster(R, a.in.units, &a.cluster, &keep);
+  int threads = 0;
+  const cudaError_t e = policy_cluster(R, a.in.units, &a.cluster, &threads, &keep);
   if (e != cudaSuccess) return e;
   a.per_part = (a.in.units + a.cluster - 1) / a.cluster;
   const bool ent = a.entropy != nullptr || a.entropy_coef != 0.0f;
-  if (out.grad_type == VSL_GRAD_BF16) return launch_policy<__nv_bfloat16>(a, R, ent, keep, stream);
-  return launch_policy<float>(a, R, ent, keep, stream);
+  if (out.grad_type == VSL_GRAD_BF16) return launch_policy<__nv_bfloat16>(a, R, threads, ent, keep, stream);
+  return launch_policy<float>(a, R, threads, ent, keep, stream);
 }
 
 }  // namespace vsl
