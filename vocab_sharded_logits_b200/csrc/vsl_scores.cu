@@ -277,7 +277,10 @@ struct LogprobArgs {
 };
 
 // A cluster per row: each CTA streams a part of the row once; the CTAs exchange
-// their sums over distributed shared memory.
+// their sums over distributed shared memory.  Bound by DRAM where there are rows
+// enough (2,048 of 151,936: 187 us, 6.6 TB/s; 512: 53 us, 5.9 TB/s, the last,
+// partial set of CTAs in it), by the chain of load, sums, exchange and the row's
+// arithmetic where there are few (64 rows of 248,320: 15 us; 4 of 1,024: 4.3 us).
 template <bool ENT, int THREADS>
 __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int kWarps = THREADS / 32;
@@ -372,6 +375,9 @@ struct LogprobGradArgs {
   int parts;               // CTAs per row
 };
 
+// Four CTAs of 512 threads an SM, each 8 units of a row a thread, two loads in
+// flight: no sum is shared, so the work is cut finely.  Bound by DRAM: 512 rows of
+// 151,936 96 us to float32 (6.5 TB/s of one read and one write), 81 us to bf16 (5.7).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) token_logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
   const int row = static_cast<int>(blockIdx.x) / a.parts;
@@ -466,6 +472,14 @@ __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int
 // over distributed shared memory, and read their parts again for the gradient,
 // out of the L2 cache: the first reading asks it to keep the lines, the second
 // and the gradient's stores to let theirs go first.
+//
+// DRAM sees the row once (512 rows of 151,936: 350 MB read of 311 without the
+// second reading, 279 MB written): 132 us to float32, 107 to bf16; 2,048 rows
+// 486 and 385 us, 5.1 and 4.9 TB/s.  What bounds it is that a row's phases wait
+// on one another (read, exchange, the row's arithmetic in 64 bits, read and
+// write): the rows beside it on the SM fill the gaps only in part.  A form that
+// kept the row in a cluster's shared memory, fed by TMA through a ring, took 588
+// us for the 2,048 rows: fewer rows at a time, longer gaps.
 template <typename T, bool ENT, bool KEEP, int THREADS>
 __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS)
     policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
@@ -620,9 +634,9 @@ int row_threads(int R, int units, bool cached, int sms) {
 // share, but not faster than a third.  Both constants are fits to measured
 // times, and only their ratio matters: it keeps, say, 148 rows from taking 4
 // CTAs each, a third more than there are places (policy loss of 148 rows of
-// 151,936: 51 us with 4, 45 with 2).  `cached`: the rows being worked on at a
+// 151,936, CTAs of 512: 51 us with 4, 45 with 2).  `cached`: the rows being worked on at a
 // time must leave the L2 cache room, at most 96 MB of its 126 (2,048 rows of
-// 151,936: 0.50 ms with 4 CTAs a row, 67 MB; 0.55 with 2, 135 MB).
+// 151,936, CTAs of 512: 0.50 ms with 4 a row, 67 MB; 0.55 with 2, 135 MB).
 cudaError_t choose_cluster(int R, int units, float per_unit, float fixed, bool cached, int* cluster, int* threads_out) {
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
@@ -652,8 +666,8 @@ cudaError_t row_cluster(int R, int units, int* cluster, int* threads) {
 
 // keep: the threads hold their parts in registers between the two passes,
 // which pays where all CTAs run at once and time is latency (4 rows of 1,024:
-// 6.3 us, 8.4 without), not where it halves how many do (300 rows of 51,012: 73
-// us, 35 without).
+// 6.3 us, 8.4 without), not where it halves how many do (300 rows of 51,012, CTAs
+// of 512: 73 us, 35 without).
 cudaError_t policy_cluster(int R, int units, int* cluster, int* threads, bool* keep) {
   const cudaError_t e = choose_cluster(R, units, 1.1f, 6.0f, true, cluster, threads);
   if (e != cudaSuccess) return e;
