@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
@@ -594,6 +595,15 @@ __device__ __forceinline__ void add_sums(float4 (&x)[2][2], const float (&d)[4][
 __device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)[2], const int (&r)[2], int j, int V_s,
                                               int t, float4 (&x)[2][2]) {
   dst += j + 4 * t;
+  if (j + 32 <= V_s) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (r[i] >= 0) {
+        *reinterpret_cast<float4*>(dst + row_at[i]) = x[i][0];
+        *reinterpret_cast<float4*>(dst + row_at[i] + 16) = x[i][1];
+      }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -660,9 +670,12 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
          (static_cast<size_t>(w.adapter >= 0 ? w.adapter : 0) * p.V_s + load_j + n_id) * p.rank + kLaneRanks * t;
   };
   place();
+  uint32_t to = smem_u32(stages) + 16 * lane;  // the stage that is copied to, this lane's 16 bytes
+  const uint32_t to_end = to + kStages * sizeof(Stage);
   auto issue = [&](int h) {
-    Stage& st = stages[h % kStages];
-    const uint32_t x_to = smem_u32(&st.x[0][lane]), b_to = smem_u32(&st.b[0][lane]);
+    const uint32_t x_to = to, b_to = to + offsetof(Stage, b) - (16 - Stage::kBytes) * lane;
+    to += sizeof(Stage);
+    if (to == to_end) to -= kStages * sizeof(Stage);
     constexpr int kB = Stage::kBytes, kRow = 32 * kB;  // a copy over the warp's lanes
     if (load_j + 32 <= p.V_s) {
       if (r[0] >= 0) {
@@ -674,19 +687,20 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
         copy_async<16, 1536, 64>(x_to, x1);
       }
       if (w.adapter >= 0) {
-        const __nv_bfloat16* id[4] = {b0, b0 + two, b0 + 8 * two, b0 + 9 * two};
         if (even_ranks) {
-          copy_async<kB, 0, 0>(b_to, id[0]);
-          copy_async<kB, kRow, 0>(b_to, id[1]);
-          copy_async<kB, 2 * kRow, 0>(b_to, id[2]);
-          copy_async<kB, 3 * kRow, 0>(b_to, id[3]);
+          constexpr int kId = 2 * 16 * STEPS;  // bytes of an id's row
+          copy_async<kB, 0, 0>(b_to, b0);
+          copy_async<kB, kRow, 2 * kId>(b_to, b0);
+          copy_async<kB, 2 * kRow, 16 * kId>(b_to, b0);
+          copy_async<kB, 3 * kRow, 18 * kId>(b_to, b0);
           if constexpr (STEPS == 4) {
-            copy_async<kB, 4 * kRow, 64>(b_to, id[0]);
-            copy_async<kB, 5 * kRow, 64>(b_to, id[1]);
-            copy_async<kB, 6 * kRow, 64>(b_to, id[2]);
-            copy_async<kB, 7 * kRow, 64>(b_to, id[3]);
+            copy_async<kB, 4 * kRow, 64>(b_to, b0);
+            copy_async<kB, 5 * kRow, 2 * kId + 64>(b_to, b0);
+            copy_async<kB, 6 * kRow, 16 * kId + 64>(b_to, b0);
+            copy_async<kB, 7 * kRow, 18 * kId + 64>(b_to, b0);
           }
         } else {
+          const __nv_bfloat16* id[4] = {b0, b0 + two, b0 + 8 * two, b0 + 9 * two};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // past the rank: zeros
             copy_async_or_zero<kB, 0, 0>(b_to + i * kRow, id[i], kLaneRanks * t < p.rank);
@@ -721,6 +735,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
     }
   };
   const int quarters = 4 * (w.last_block - w.block0);
+  const Stage* at = stages;  // the stage that is read
 #pragma unroll
   for (int h = 0; h < kStages - 1; ++h) {
     issue(h);  // (a warp has four quarters at least)
@@ -733,7 +748,8 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
     if (h + kStages - 1 < quarters) issue(h + kStages - 1);
     copy_commit();  // a group a quarter, empty ones at the end
     copy_wait<kStages - 1>();
-    const Stage& st = stages[h % kStages];
+    const Stage& st = *at;
+    if (++at == stages + kStages) at = stages;
     const int j = in_slice * 128 + 32 * (h & 3);
     float4 x[2][2];
     float d[4][4];
