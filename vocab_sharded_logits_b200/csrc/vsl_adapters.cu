@@ -41,7 +41,7 @@ namespace {
 constexpr int kUnitRows = 16;     // rows per tensor-core product
 constexpr int kTile = 256;        // rows sorted together
 constexpr int kShrinkWarps = 8;   // kShrinkWarps * 32 == kTile: a thread sorts a row
-constexpr int kExpandWarps = 4;
+constexpr int kWideWarps = 4;     // most warps of a CTA of the second kernel
 constexpr int kTerms = 3;         // bf16 terms of u
 constexpr int kFragment = 32 * 4; // 32-bit registers of one A operand (16 x 16 bf16) over a warp
 constexpr int kMaxSplit = 4;      // CTAs that share H
@@ -531,10 +531,10 @@ struct ExpandStage {
 constexpr int kStages = 3;
 template <int STEPS>
 constexpr size_t expand_smem() {
-  return kExpandWarps * kStages * sizeof(ExpandStage<STEPS>);
+  return kStages * sizeof(ExpandStage<STEPS>);
 }
 // CTAs that the stages and the registers let stand on an SM.
-constexpr int expand_ctas(int steps) { return steps == 4 ? 3 : 4; }
+constexpr int expand_ctas(int steps) { return steps == 4 ? 12 : 16; }
 
 // A warp's unit: its plan entry, and where its u is.
 struct WarpUnit {
@@ -543,9 +543,9 @@ struct WarpUnit {
   int adapter, count, block0, last_block;
   bool work;
 };
-__device__ __forceinline__ WarpUnit warp_unit(const ExpandArgs& p, int warp, int steps) {
+__device__ __forceinline__ WarpUnit warp_unit(const ExpandArgs& p, int warp, int warps, int steps) {
   WarpUnit w{};
-  const int item = static_cast<int>(blockIdx.x % p.slot_ctas) * kExpandWarps + warp;
+  const int item = static_cast<int>(blockIdx.x % p.slot_ctas) * warps + warp;
   w.block0 = static_cast<int>(blockIdx.x / p.slot_ctas) * p.warp_blocks;
   w.last_block = min(w.block0 + p.warp_blocks, p.S * p.B);
   const int tile = item / p.slots, slot = item - tile * p.slots;
@@ -615,7 +615,11 @@ __device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)
     }
 }
 
-// A warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice), a
+// A CTA is one warp: a unit whose rows are few, or a slot that is empty, holds no
+// other warp's place (one row of rank 16: 8.3 us, 10.4 with four warps a CTA; 64
+// requests 76 us, 78).
+//
+// The warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice), a
 // quarter at a time, the next quarters' logits and B on their way meanwhile.
 // The products' N index is laid over the ids so that a lane's sums are 4
 // consecutive ids of a row: column n of the i-th product of 4 is id
@@ -629,13 +633,12 @@ __device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)
 // bounds it (fewer instructions, more warps or more stages left the time where
 // it was; B through L1 cost 10 %).
 template <int STEPS, int LANES>  // rank_steps, lanes of 8 ranks in few_rows (0: no unit comes there)
-__global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
+__global__ void __launch_bounds__(32, expand_ctas(STEPS))
     adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
   extern __shared__ uint4 expand_stages[];
   using Stage = ExpandStage<STEPS>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const WarpUnit w = warp_unit(p, warp, STEPS);
+  const int lane = threadIdx.x, g = lane >> 2, t = lane & 3;
+  const WarpUnit w = warp_unit(p, 0, 1, STEPS);
   if (!w.work) return;
   if constexpr (LANES > 0) {
     if (w.adapter >= 0 && w.count <= kFewRows) {  // the whole warp's
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
       return;
     }
   }
-  Stage* stages = reinterpret_cast<Stage*>(expand_stages) + warp * kStages;
+  Stage* stages = reinterpret_cast<Stage*>(expand_stages);
   const int r[2] = {w.entry[4 + g], w.entry[4 + g + 8]};
   const size_t row_at[2] = {static_cast<size_t>(max(r[0], 0)) * p.V_s, static_cast<size_t>(max(r[1], 0)) * p.V_s};
   uint4 u[STEPS * kTerms];
@@ -810,11 +813,11 @@ __global__ void __launch_bounds__(kExpandWarps * 32, expand_ctas(STEPS))
 // The same for ranks above 64: B and u are loaded as they are used, so that the
 // time is the loads' latency over the warps that stand on an SM (512 rows over 8
 // adapters: 321 us at rank 128, 526 at rank 256; 3.0 and 2.4 TB/s).
-__global__ void __launch_bounds__(kExpandWarps * 32, 4) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
+__global__ void __launch_bounds__(kWideWarps * 32, 16 / kWideWarps) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int steps = rank_steps(p.rank);
-  const WarpUnit w = warp_unit(p, warp, steps);
+  const WarpUnit w = warp_unit(p, warp, static_cast<int>(blockDim.x >> 5), steps);
   if (!w.work) return;
   const int r[2] = {w.entry[4 + g], w.entry[4 + g + 8]};
   const size_t row_at[2] = {static_cast<size_t>(max(r[0], 0)) * p.V_s, static_cast<size_t>(max(r[1], 0)) * p.V_s};
@@ -893,11 +896,12 @@ AdapterSizes adapter_sizes(int R, int n, int rank) {
 
 // The second kernel: may start before the one ahead of it ends, waits for its
 // results itself.
-cudaError_t launch_after(void (*kernel)(ExpandArgs), const ExpandArgs& a, unsigned grid, size_t smem, cudaStream_t stream) {
+cudaError_t launch_after(void (*kernel)(ExpandArgs), const ExpandArgs& a, unsigned grid, int warps, size_t smem,
+                         cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kExpandWarps * 32);
+  cfg.blockDim = dim3(warps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -919,9 +923,15 @@ cudaError_t prepare_expand() {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   std::call_once(once[dev], [&] {
+    constexpr int kCarveout = 72;  // percent: 164 KB
     const auto allow = [&](void (*kernel)(ExpandArgs), size_t smem) {
       if (status[dev] == cudaSuccess)
         status[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      // The rest is L1, which the multiply-adds' loads need (64 requests of rank
+      // 32: 129 us, 148 with 196 KB; of rank 16 76 us, 90), and no case wants
+      // more warps than fit (2,048 rows of rank 64: 591 us, 595 with 228 KB).
+      if (status[dev] == cudaSuccess)
+        status[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
     };
     status[dev] = cudaSuccess;
     allow(adapters_expand_kernel<1, 1>, expand_smem<1>());
@@ -994,25 +1004,29 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   ea.B = (V_s + 127) / 128;
   ea.slots = z.slots;
   ea.tiles = z.tiles;
-  ea.slot_ctas = static_cast<int>((static_cast<long long>(z.tiles) * z.slots + kExpandWarps - 1) / kExpandWarps);
+  // Above rank 64 the warps of a CTA, next units, read the same B out of L1 where
+  // adapters have units enough (512 rows over 8 adapters of rank 128: 325 us, 338
+  // by single warps; 16 over 16: 146, 142; one row of rank 256: 43, 29).
+  const int warps = rank > 64 && R > kUnitRows * static_cast<long long>(n) ? kWideWarps : 1;
+  ea.slot_ctas = static_cast<int>((static_cast<long long>(z.tiles) * z.slots + warps - 1) / warps);
   // A warp keeps its unit's u over several blocks, while there are warps enough
   // to fill the SMs some times over (64 requests of rank 16: 78 us, 94 with a
   // block a warp; 2,048 rows over 8 adapters of rank 64: 620 us, 712).  Above
   // rank 64 it keeps no u (512 rows of rank 256: 545 us, 577 with several blocks).
   ea.warp_blocks = 1;
-  while (rank <= 64 && ea.warp_blocks < 8 && static_cast<long long>(ea.slot_ctas) * S * ea.B / ea.warp_blocks > 8 * 148 * 4)
+  while (rank <= 64 && ea.warp_blocks < 8 && static_cast<long long>(ea.slot_ctas) * S * ea.B / ea.warp_blocks > 8 * 148 * 16)
     ea.warp_blocks *= 2;
   const long long grid =
       static_cast<long long>(ea.slot_ctas) * ((static_cast<long long>(S) * ea.B + ea.warp_blocks - 1) / ea.warp_blocks);
   if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   const unsigned g = static_cast<unsigned>(grid);
-  if (rank > 64) return launch_after(adapters_expand_wide_kernel, ea, g, 0, stream);
+  if (rank > 64) return launch_after(adapters_expand_wide_kernel, ea, g, warps, 0, stream);
   const cudaError_t e = prepare_expand();
   if (e != cudaSuccess) return e;
-  if (rank > 32) return launch_after(adapters_expand_kernel<4, 0>, ea, g, expand_smem<4>(), stream);
-  if (rank > 16) return launch_after(adapters_expand_kernel<2, 4>, ea, g, expand_smem<2>(), stream);
-  if (rank > 8) return launch_after(adapters_expand_kernel<1, 2>, ea, g, expand_smem<1>(), stream);
-  return launch_after(adapters_expand_kernel<1, 1>, ea, g, expand_smem<1>(), stream);
+  if (rank > 32) return launch_after(adapters_expand_kernel<4, 0>, ea, g, 1, expand_smem<4>(), stream);
+  if (rank > 16) return launch_after(adapters_expand_kernel<2, 4>, ea, g, 1, expand_smem<2>(), stream);
+  if (rank > 8) return launch_after(adapters_expand_kernel<1, 2>, ea, g, 1, expand_smem<1>(), stream);
+  return launch_after(adapters_expand_kernel<1, 1>, ea, g, 1, expand_smem<1>(), stream);
 }
 
 }  // namespace vsl
