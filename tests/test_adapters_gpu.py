@@ -256,3 +256,18 @@ def test_from_projection_to_gradient(cuda_device):
     bound = B.grad_bound(logp, tokens, 1.0, dl, 0 * dl, np.abs(dl) * 2.0 ** -23, 0 * dl, want_g, "fp32")
     assert (np.abs(np.concatenate([_np(x) for x in grad], 1) - want_g) <= bound).all()
     assert V == l64.shape[1] and vsl.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64])
+def test_small_terms_survive_a_cancelled_logit(cuda_device, rank):
+    """u = 1 + 2^-10 + 2^-20, B = 1 + 2^-7: the product has 28 bits, and the base logit takes the first away."""
+    R, H, V_s = 20, 8, 260
+    hidden = torch.zeros(R, H)
+    hidden[:, 0], hidden[:, 1], hidden[:, 2] = 1.0, 2.0 ** -10, 2.0 ** -20
+    a, b = torch.zeros(1, rank, H), torch.zeros(1, V_s, rank)
+    a[0, 0, :3], b[0, :, 0] = 1.0, 1 + 2.0 ** -7
+    bf16 = lambda x: x.to(cuda_device, torch.bfloat16)  # noqa: E731
+    logits = torch.full((R, V_s), -(1 + 2.0 ** -7), device=cuda_device)
+    ids = torch.zeros(R, dtype=torch.int32, device=cuda_device)
+    out, = vsl.adapters_add([logits], bf16(hidden), bf16(a), [bf16(b)], ids)
+    assert bool((out == 2.0 ** -10 + 2.0 ** -17 + 2.0 ** -20 + 2.0 ** -27).all())

@@ -533,8 +533,9 @@ template <int STEPS>
 constexpr size_t expand_smem() {
   return kStages * sizeof(ExpandStage<STEPS>);
 }
-// CTAs that the stages and the registers let stand on an SM.
-constexpr int expand_ctas(int steps) { return steps == 4 ? 12 : 16; }
+// CTAs that the registers let stand on an SM (512 rows of rank 32 with statistics:
+// 189 us with 13, 204 with 16, 225 with 12, rank 64 no different with fewer).
+constexpr int expand_ctas(int steps) { return steps == 4 ? 12 : steps == 2 ? 13 : 16; }
 
 // A warp's unit: its plan entry, and where its u is.
 struct WarpUnit {
@@ -563,31 +564,37 @@ __device__ __forceinline__ WarpUnit warp_unit(const ExpandArgs& p, int warp, int
 }
 
 // A step's products of 32 ids: y, a lane's B of the four products; a, u's
-// operands of the step; FIRST: the sums begin with it.
-template <bool FIRST>
-__device__ __forceinline__ void step_products(float (&d)[4][4], const uint4 (&a)[kTerms], const uint2 (&y)[4]) {
+// operands of the step; FIRST: the sums begin with it.  ACC = 2: the large
+// term's sums and the two small ones' apart.
+template <bool FIRST, int ACC>
+__device__ __forceinline__ void step_products(float (&d)[ACC][4][4], const uint4 (&a)[kTerms], const uint2 (&y)[4]) {
 #pragma unroll
   for (int e = 0; e < kTerms; ++e)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (FIRST && e == 0)
-        mma_16816_first(d[i], a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
+      float(&to)[4] = d[e == 0 ? 0 : ACC - 1][i];
+      if (FIRST && e < ACC)
+        mma_16816_first(to, a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
       else
-        mma_16816(d[i], a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
+        mma_16816(to, a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
     }
 }
 
-// The sums of 32 ids onto the rows' logits.
-__device__ __forceinline__ void add_sums(float4 (&x)[2][2], const float (&d)[4][4]) {
+// The sums of 32 ids onto the rows' logits, the large terms' first: where those
+// cancel the logit the sum is exact, and the small terms are what is left.
+template <int ACC>
+__device__ __forceinline__ void add_sums(float4 (&x)[2][2], const float (&d)[ACC][4][4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int e = 0; e < ACC; ++e)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      x[i][b].x += d[2 * b][2 * i];
-      x[i][b].y += d[2 * b][2 * i + 1];
-      x[i][b].z += d[2 * b + 1][2 * i];
-      x[i][b].w += d[2 * b + 1][2 * i + 1];
-    }
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        x[i][b].x += d[e][2 * b][2 * i];
+        x[i][b].y += d[e][2 * b][2 * i + 1];
+        x[i][b].z += d[e][2 * b + 1][2 * i];
+        x[i][b].w += d[e][2 * b + 1][2 * i + 1];
+      }
 }
 
 // Stores a quarter of the unit's rows, j its first id; a lane's logits past the
@@ -755,7 +762,7 @@ __global__ void __launch_bounds__(32, expand_ctas(STEPS))
     if (++at == stages + kStages) at = stages;
     const int j = in_slice * 128 + 32 * (h & 3);
     float4 x[2][2];
-    float d[4][4];
+    float d[2][4][4];
     if (w.adapter >= 0) {
       if constexpr (STEPS == 1) {
         uint2 y[4];
@@ -838,7 +845,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, 16 / kWideWarps) adapters_exp
     if (w.adapter >= 0) {
       const __nv_bfloat16* id0 = p.b[slice] + (static_cast<size_t>(w.adapter) * p.V_s + j + n_id) * p.rank + 8 * t;
       const int most = p.V_s - 1 - j - n_id;  // ids past the slice's end take its last one's row instead
-      float d[4][4] = {};
+      float d[1][4][4] = {};
 #pragma unroll 2
       for (int k = 0; k < steps; k += 2) {
         uint2 y0[4], y1[4];
