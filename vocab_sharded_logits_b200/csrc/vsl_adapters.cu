@@ -19,10 +19,10 @@
 // What it cannot do without: one read and one write of the logits and one read
 // of each used adapter's A and B.  Measured (H = 4,096 but where stated, of the
 // time those bytes take at the 6.56 TB/s of a copy): one row of rank 16 over
-// 151,936 ids 10.3 us (two launches, one of which waits for the other's end);
-// 64 rows of as many adapters of rank 16 78.6 us, 77 %; 512 rows over 24
-// adapters of rank 32 171 us, 198 with tile statistics, 64 %; 2,048 rows over 8
-// adapters of rank 64 (H = 5,120) 685 us, 59 %.
+// 151,936 ids 8.3 us (two launches, one of which waits for the other's end); 64
+// rows of as many adapters of rank 16 76 us, 80 %; 512 rows over 24 adapters of
+// rank 32 167 us, 189 with tile statistics, 67 %; 2,048 rows over 8 adapters of
+// rank 64 (H = 5,120) 675 us, 60 %.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -105,7 +105,7 @@ struct ShrinkArgs {
 // part, the CTAs of a cluster share H.  Every CTA sorts the tile itself, by
 // counting, which costs less than a launch that does it once.  Bound by the
 // latency of its chain (ids, sort, one run over H, the warps' sums, the
-// cluster's): 21 us for 512 rows over 24 adapters of rank 32, 43 us for 2,048
+// cluster's): 21 us for 512 rows over 24 adapters of rank 32, 42 us for 2,048
 // over 8 of rank 64 (H = 5,120); the second kernel's CTAs are already there when
 // it ends.
 __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(const __grid_constant__ ShrinkArgs p) {
@@ -632,13 +632,14 @@ __device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)
 // consecutive ids of a row: column n of the i-th product of 4 is id
 // 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.
 //
-// 512 rows over 24 adapters of rank 32 with statistics: 190 us, 0.79 GB of DRAM
-// traffic (4.1 TB/s), the issue slots 55 % used: 12 warps an SM that each wait on
-// chains of their own.  2,048 rows over 8 adapters of rank 64: 575 us, 2.64 GB
-// (4.6 TB/s), the tensor pipe 44 % active, and 7.5 GB through the L2 cache, where
-// the B's of 155 MB are read once for each unit of 16 rows: that traffic is what
-// bounds it (fewer instructions, more warps or more stages left the time where
-// it was; B through L1 cost 10 %).
+// 512 rows over 24 adapters of rank 32 with statistics: 171 us, 0.78 GB of DRAM
+// traffic (4.6 TB/s), the issue slots 56 % used.  2,048 rows over 8 adapters of
+// rank 64: 559 us, 2.64 GB (4.7 TB/s), the tensor pipe 45 % active, 7.5 GB
+// through the L2 cache, where the B's of 155 MB are read once for each unit of
+// 16 rows.  No unit is full; what is left is their overlap within a warp, which
+// waits for copies, products and sums in turn.  Units of 32 rows, which read B
+// half as often, need twice the registers: 612 us where this takes 591; more
+// warps, more stages or B through L1 left the time as it was or cost up to 10 %.
 template <int STEPS, int LANES>  // rank_steps, lanes of 8 ranks in few_rows (0: no unit comes there)
 __global__ void __launch_bounds__(32, expand_ctas(STEPS))
     adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(32, expand_ctas(STEPS))
 
 // The same for ranks above 64: B and u are loaded as they are used, so that the
 // time is the loads' latency over the warps that stand on an SM (512 rows over 8
-// adapters: 321 us at rank 128, 526 at rank 256; 3.0 and 2.4 TB/s).
+// adapters: 325 us at rank 128, 526 at rank 256; 2.9 and 2.4 TB/s).
 __global__ void __launch_bounds__(kWideWarps * 32, 16 / kWideWarps) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
