@@ -132,6 +132,16 @@ at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device d) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(d));
 }
 
+// A contiguous piece of a fresh tensor as a tensor of its own over the same
+// storage (a view without the dispatcher, which takes a microsecond).
+at::Tensor piece(const at::Tensor& whole, int64_t first, at::IntArrayRef shape) {
+  at::Tensor t =
+      at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(first);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 PyObject* wrap(const at::Tensor& t) {
   PyObject* o = THPVariable_Wrap(t);
   if (o == nullptr) throw Raised();
@@ -169,10 +179,11 @@ struct OutSlices {
     list = PyList_New(in.S);
     if (list == nullptr) throw Raised();
     const bool one = static_cast<int64_t>(in.R) * in.V_s % 8 == 0;
-    std::vector<at::Tensor> parts;
-    if (one) parts = empty({in.S, in.R, in.V_s}, type, in.device).unbind(0);
+    const int64_t entries = static_cast<int64_t>(in.R) * in.V_s;
+    at::Tensor all;
+    if (one) all = empty({in.S * entries}, type, in.device);
     for (int s = 0; s < in.S; ++s) {
-      const at::Tensor t = one ? std::move(parts[s]) : empty({in.R, in.V_s}, type, in.device);
+      const at::Tensor t = one ? piece(all, s * entries, {in.R, in.V_s}) : empty({in.R, in.V_s}, type, in.device);
       at.push_back(t.data_ptr());
       PyList_SET_ITEM(list, s, wrap(t));
     }
@@ -280,7 +291,7 @@ PyObject* policy_loss(PyObject* const* a, Py_ssize_t n) {
   i.temperature = static_cast<float>(number(a[10]));
   need_cuda(in.device);
   const bool with_grad = a[11] != Py_False;
-  at::Tensor rows = empty({4, in.R}, at::kFloat, in.device);
+  const at::Tensor rows = empty({4 * static_cast<int64_t>(in.R)}, at::kFloat, in.device);
   float* at = rows.data_ptr<float>();
   vsl_policy_outputs o{};
   o.loss = at;
@@ -310,8 +321,7 @@ PyObject* policy_loss(PyObject* const* a, Py_ssize_t n) {
     Py_INCREF(grad_list);
   }
   PyTuple_SET_ITEM(result, 4, grad_list);
-  const std::vector<at::Tensor> outputs = rows.unbind(0);
-  for (int k = 0; k < 4; ++k) PyTuple_SET_ITEM(result, k, wrap(outputs[k]));
+  for (int k = 0; k < 4; ++k) PyTuple_SET_ITEM(result, k, wrap(piece(rows, k * static_cast<int64_t>(in.R), {in.R})));
   return result;
 }
 

@@ -690,7 +690,7 @@ cudaError_t launch_clusters(void (*kernel)(Args), const Args& a, int R, int clus
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
