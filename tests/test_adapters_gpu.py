@@ -50,6 +50,8 @@ def _check(out, logits, hidden, a, b, ids, scale):
     (600, 64, 16, 132, 9, 32),     # three tiles of rows, blocks over many slices
     (300, 1040, 2, 1000, 40, 64),  # H shared by a cluster, ragged units
     (280, 72, 3, 20, 4, 56),       # slices of less than a block
+    (100, 72, 2, 388, 2, 128),     # ranks above 64, several units an adapter
+    (300, 64, 1, 260, 1, 200),
 ])
 def test_parity(cuda_device, R, H, S, V_s, n, rank):
     hidden, logits, a, b, scale, ids = _inputs(R, H, S, V_s, n, rank, R + rank, cuda_device)

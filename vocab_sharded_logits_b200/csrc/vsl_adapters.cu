@@ -41,7 +41,7 @@ namespace {
 constexpr int kUnitRows = 16;     // rows per tensor-core product
 constexpr int kTile = 256;        // rows sorted together
 constexpr int kShrinkWarps = 8;   // kShrinkWarps * 32 == kTile: a thread sorts a row
-constexpr int kWideWarps = 4;     // most warps of a CTA of the second kernel
+constexpr int kWideWarps = 4;     // most warps of a CTA of the second kernel above rank 64
 constexpr int kTerms = 3;         // bf16 terms of u
 constexpr int kFragment = 32 * 4; // 32-bit registers of one A operand (16 x 16 bf16) over a warp
 constexpr int kMaxSplit = 4;      // CTAs that share H
