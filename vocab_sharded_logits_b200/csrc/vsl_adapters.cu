@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
     if (tid == kUnitRows + 1) entry[1] = count;
   }
   if (adapter < 0) return;
+  cluster_arrive();  // this CTA runs; waited for before the first access to another's memory
 
   // ---- u of the unit: 16 rows x kRanks ranks
   const int g = lane >> 2, t = lane & 3;
@@ -220,6 +221,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
     }
     __syncthreads();
   }
+  cluster_wait();  // every CTA of the cluster runs
   for (int e = tid; e < kUnitRows * kRanks; e += kShrinkWarps * 32) {
     float u = 0.0f;
 #pragma unroll

@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
     }
     return;
   }
+  cluster_arrive();  // this CTA runs; waited for before the first access to another's memory
   const float logit = warp == 0 ? token_logit(a.in, row, token) : 0.0f;
   const int first = min(a.in.units, rank * a.per_part), last = min(a.in.units, first + a.per_part);
   const uint64_t policy = policy_evict_first();
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
   }
   fast_warp_sums<ENT>(s, warps, warp, lane);
   __syncthreads();
+  cluster_wait();  // every CTA of the cluster runs
   if (warp == 0) {
     const PartStats p = fast_part<ENT, kWarps>(warps, lane, k);
     if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
@@ -508,6 +510,7 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     if (a.grad) part_grad<T>(a.in, a.out, off, row, first, last, threadIdx.x, THREADS);
     return;
   }
+  cluster_arrive();  // this CTA runs; waited for before the first access to another's memory
   RowInputs in{};
   if (warp == 0) in = row_inputs(a, row, token);
   const uint64_t keep = KEEP ? policy_evict_first() : policy_evict_last();
@@ -531,6 +534,7 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
   }
   fast_warp_sums<ENT>(s, warps, warp, lane);
   __syncthreads();
+  cluster_wait();  // every CTA of the cluster runs
   if (warp == 0) {
     const PartStats p = fast_part<ENT, kWarps>(warps, lane, k);
     if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
