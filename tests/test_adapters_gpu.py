@@ -273,3 +273,27 @@ def test_small_terms_survive_a_cancelled_logit(cuda_device, rank):
     ids = torch.zeros(R, dtype=torch.int32, device=cuda_device)
     out, = vsl.adapters_add([logits], bf16(hidden), bf16(a), [bf16(b)], ids)
     assert bool((out == 2.0 ** -10 + 2.0 ** -17 + 2.0 ** -20 + 2.0 ** -27).all())
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("per", [1, 2, 3])
+@pytest.mark.parametrize("V_s", [132, 260, 388])
+def test_statistics_of_a_slice_that_ends_in_an_infinity(cuda_device, V_s, per, rank):
+    """The last id's product overflows to +inf; what is behind it in its block belongs to no id."""
+    R = 6 * per
+    hidden, logits, a, b, scale, ids = _inputs(R, 64, 2, V_s, 6, rank, rank + per, cuda_device, np.arange(R) // per)
+    hidden[:, 0] = 2.0 ** 126
+    a[:, :, 0] = 0.0
+    a[:, 0] = 0.0
+    a[:, 0, 0] = 1.0                                      # u = 2^126 in the first rank alone
+    for x in b:
+        x[:, :, 0] = 0.0
+        x[:, V_s - 1, 0] = 8.0
+    out, stats = vsl.adapters_add(logits, hidden, a, b, ids, tile_stats=True)
+    assert all(bool((x[:, -1] == float("inf")).all()) and bool(torch.isfinite(x[:, :-1]).all()) for x in out)
+    ref = vsl.tile_stats(out)
+    assert torch.equal(stats[..., :4], ref[..., :4]) and torch.equal(stats[..., 5:], ref[..., 5:])
+    s, r = stats[..., 4], ref[..., 4]
+    bad = ~torch.isfinite(r)
+    assert bool((s[bad] == r[bad]).all())                 # +inf, no NaN
+    assert bool(((s - r).abs() <= r * 2 * (2.0 ** -22 + 2.0 ** -19 + 2.0 ** -17))[~bad].all())

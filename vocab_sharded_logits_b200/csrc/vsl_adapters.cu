@@ -489,7 +489,12 @@ __device__ __forceinline__ void few_rows(const ExpandArgs& p, int adapter, const
         for (int m = 0; m < 4; ++m)
           if (32 * m + mine <= most)
             p.out[slice][static_cast<size_t>(row[c]) * p.V_s + j0 + 32 * m + mine] = v[c][m];
-        if (p.stats != nullptr) warp_stats(v[c], p.stats + (static_cast<size_t>(row[c]) * p.S * p.B + block) * 8, lane);
+        if (p.stats != nullptr) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)  // past the slice's end: -inf again, where an infinite product made it a NaN
+            if (32 * m + mine > most) v[c][m] = -INFINITY;
+          warp_stats(v[c], p.stats + (static_cast<size_t>(row[c]) * p.S * p.B + block) * 8, lane);
+        }
       }
   }
 }
