@@ -297,3 +297,19 @@ def test_statistics_of_a_slice_that_ends_in_an_infinity(cuda_device, V_s, per, r
     bad = ~torch.isfinite(r)
     assert bool((s[bad] == r[bad]).all())                 # +inf, no NaN
     assert bool(((s - r).abs() <= r * 2 * (2.0 ** -22 + 2.0 ** -19 + 2.0 ** -17))[~bad].all())
+
+
+@pytest.mark.parametrize("rank", [72, 128, 200, 256])
+def test_small_terms_survive_a_cancelled_logit_above_rank_64(cuda_device, rank):
+    """The same, with the ranks that count at both ends of the sum."""
+    R, H, V_s = 20, 8, 260
+    hidden = torch.zeros(R, H)
+    hidden[:, 0], hidden[:, 1], hidden[:, 2] = 1.0, 2.0 ** -10, 2.0 ** -20
+    for k in (0, rank // 2, rank - 1):
+        a, b = torch.zeros(1, rank, H), torch.zeros(1, V_s, rank)
+        a[0, k, :3], b[0, :, k] = 1.0, 1 + 2.0 ** -7
+        bf16 = lambda x: x.to(cuda_device, torch.bfloat16)  # noqa: E731
+        logits = torch.full((R, V_s), -(1 + 2.0 ** -7), device=cuda_device)
+        ids = torch.zeros(R, dtype=torch.int32, device=cuda_device)
+        out, = vsl.adapters_add([logits], bf16(hidden), bf16(a), [bf16(b)], ids)
+        assert bool((out == 2.0 ** -10 + 2.0 ** -17 + 2.0 ** -20 + 2.0 ** -27).all())

@@ -827,7 +827,9 @@ __global__ void __launch_bounds__(32, expand_ctas(STEPS))
 
 // The same for ranks above 64: B and u are loaded as they are used, so that the
 // time is the loads' latency over the warps that stand on an SM (512 rows over 8
-// adapters: 325 us at rank 128, 526 at rank 256; 2.9 and 2.4 TB/s).
+// adapters: 354 us at rank 128, 590 at rank 256; 2.6 and 2.1 TB/s).  The small
+// terms' sums stay apart here too; their 16 registers cost a tenth (324 and 525
+// us in one sum, which loses them where the large terms cancel the logit).
 __global__ void __launch_bounds__(kWideWarps * 32, 16 / kWideWarps) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -853,7 +855,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, 16 / kWideWarps) adapters_exp
     if (w.adapter >= 0) {
       const __nv_bfloat16* id0 = p.b[slice] + (static_cast<size_t>(w.adapter) * p.V_s + j + n_id) * p.rank + 8 * t;
       const int most = p.V_s - 1 - j - n_id;  // ids past the slice's end take its last one's row instead
-      float d[1][4][4] = {};
+      float d[2][4][4] = {};
 #pragma unroll 2
       for (int k = 0; k < steps; k += 2) {
         uint2 y0[4], y1[4];
