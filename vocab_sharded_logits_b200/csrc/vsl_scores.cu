@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 512;       // of a CTA of the gradient kernel
 constexpr int kRowThreads = 1536;   // threads of a row kernel that stand on an SM (40 registers each)
+constexpr int kLogprobThreads = 1280;  // at least as many of the logprobs' stand on an SM (48 registers)
 constexpr int kBatch = 4;      // units of four logits a thread has in flight
 constexpr int kMaxCluster = 8;
 
@@ -66,23 +67,63 @@ struct UnitReader {
   }
 };
 
+// The token, where it is one of the thread's own among units [first, last), else
+// -1 (threads: a power of two).
+__device__ __forceinline__ int own_token(int token, int first, int last, int thread, int threads) {
+  const int u = token >> 2;
+  return u >= first && u < last && ((u - first) & (threads - 1)) == thread ? token : -1;
+}
+// Puts `value` in the own token's place in the batch whose first unit is i;
+// returns what stood there.
+__device__ __forceinline__ float swap_token(float4 (&v)[kBatch], int own, int i, int step, float value) {
+  float old = value;
+  const int unit = own >> 2;
+  if (unit >= i && unit < i + kBatch * step) {  // rare; never for -1
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (unit == i + u * step) {
+        const int j = own & 3;
+        old = j == 0 ? v[u].x : j == 1 ? v[u].y : j == 2 ? v[u].z : v[u].w;
+        v[u] = make_float4(j == 0 ? value : v[u].x, j == 1 ? value : v[u].y, j == 2 ? value : v[u].z, j == 3 ? value : v[u].w);
+      }
+  }
+  return old;
+}
+
 // A CTA's threads bring their sums together: each warp's into shared memory,
-// then warp 0 (after a barrier) adds them up.
+// then warp 0 (after a barrier) adds them up.  k0: the exponent the threads
+// began with.
+struct WarpSums {
+  float z, w, k;
+};
 template <bool ENT>
-__device__ __forceinline__ void fast_warp_sums(const FastSums& s, float2* shared, int warp, int lane) {
+__device__ __forceinline__ void fast_warp_sums(FastSums s, float k, float k0, WarpSums* shared, int warp, int lane) {
+  const float top = __all_sync(0xFFFFFFFFu, k == k0) ? k0 : warp_max(k);
+  if (k != top) fast_rebase<ENT>(s, k, top);
   const float z = warp_sum(s.z.x + s.z.y);
   const float w = ENT ? warp_sum(s.w.x + s.w.y) : 0.0f;
-  if (lane == 0) shared[warp] = make_float2(z, w);
+  if (lane == 0) shared[warp] = WarpSums{z, w, top};
 }
 template <bool ENT, int WARPS>
-__device__ __forceinline__ PartStats fast_part(const float2* shared, int lane, float k) {
-  PartStats p{0.0, 0.0, k};
+__device__ __forceinline__ PartStats fast_part(const WarpSums* shared, int lane) {
+  static_assert(WARPS <= 16, "lanes 0 .. 15 hold the result");
+  PartStats p{0.0, 0.0, -FLT_MAX};
   if (lane < WARPS) {
-    p.z = shared[lane].x;
-    p.w = shared[lane].y;
+    p.z = shared[lane].z;
+    p.w = shared[lane].w;
+    p.ref = shared[lane].k;
+  }
+  float ref = p.ref;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
+  if (p.ref != ref) {
+    const double d = fmax(static_cast<double>(p.ref) - static_cast<double>(ref), -2000.0), f = exp2_int(d);
+    p.w = (p.w + d * p.z) * f;
+    p.z *= f;
+    p.ref = ref;
   }
 #pragma unroll
-  for (int o = WARPS > 16 ? 16 : 8; o > 0; o >>= 1) {
+  for (int o = 8; o > 0; o >>= 1) {
     p.z += __shfl_xor_sync(0xFFFFFFFFu, p.z, o);
     if (ENT) p.w += __shfl_xor_sync(0xFFFFFFFFu, p.w, o);
   }
@@ -90,16 +131,19 @@ __device__ __forceinline__ PartStats fast_part(const float2* shared, int lane, f
   return p;
 }
 
-// The careful sums of units [first, last) by `warps` warps, whose first lane
-// leaves them in `shared`.
-__device__ __noinline__ void careful_warp_sums(const SliceArgs& a, int row, int first, int last, int thread,
+// The careful sums of units [first, last) but the token, by `threads` threads;
+// each warp's first lane leaves them in `shared`.
+__device__ __noinline__ void careful_warp_sums(const SliceArgs& a, int row, int token, int first, int last, int thread,
                                                int threads, CarefulSums* shared) {
   UnitReader reader(a, first, last, thread, threads);
   CarefulSums s = careful_empty();
   const uint64_t policy = policy_evict_last();
+  const int own = own_token(token, first, last, thread, threads);
   while (reader.i < last) {
     float4 v[kBatch];
+    const int i = reader.i;
     reader.load(a, row, v, policy);
+    swap_token(v, own, i, threads, -INFINITY);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) careful_add(s, v[u], a.c);
   }
@@ -155,30 +199,25 @@ __device__ __forceinline__ void store_unit(__nv_bfloat16* p, const float4& g, ui
   stg_hint2(p, reinterpret_cast<uint32_t&>(lo), reinterpret_cast<uint32_t&>(hi), policy);
 }
 
-// A row's gradient coefficients for one CTA's exponentials (see the file's
-// head): G_j = e_j (alpha + gamma y_j) + at_token 1[j = token], where y_j is
-// what e_j is taken from: the exponent c l_j - ref of 2 (fast), or l_j - ref
-// (careful).
+// A row's gradient coefficients (see the file's head): G_j = e_j (alpha + gamma
+// y_j) + at_token 1[j = token], where y_j is what e_j is taken from: the exponent
+// c l_j - ref of 2 (fast), or l_j - ref (careful).
 struct GradCoef {
   float ref, alpha, gamma, at_token;
   int token;  // -1: the row does not count, its gradient is 0
   int careful;
 };
 
-// From df / dlogp = g and df / dH = h; `up`: the CTA's reference less the
-// row's (fast: an integer <= 0), ref: the CTA's reference.
+// From df / dlogp = g and df / dH = h.
 template <bool FAST>
-__device__ __forceinline__ GradCoef grad_coef(double g, double h, double z, double log_z, double entropy, double up,
-                                              float ref, const ExpScale& c, int token) {
+__device__ __forceinline__ GradCoef grad_coef(double g, double h, double z, double log_z, double entropy, float ref,
+                                              const ExpScale& c, int token) {
   GradCoef k;
   k.ref = ref;
   k.token = token;
   k.careful = !FAST;
-  // 1 / z of the exponentials as they are computed, relative to the CTA's reference
-  double f = kExpMean / z;
-  if (FAST) f *= exp2_int(up);
-  f *= -c.inv_t;
-  k.alpha = static_cast<float>(f * (h != 0.0 ? g + h * (entropy - log_z + up * kLn2) : g));
+  const double f = -c.inv_t * kExpMean / z;  // 1 / z of the exponentials as they are computed
+  k.alpha = static_cast<float>(f * (h != 0.0 ? g + h * (entropy - log_z) : g));
   k.gamma = h != 0.0 ? static_cast<float>(f * h * (FAST ? kLn2 : c.inv_t)) : 0.0f;
   k.at_token = static_cast<float>(g * c.inv_t);
   return k;
@@ -266,6 +305,11 @@ __device__ __forceinline__ void part_grad(const SliceArgs& a, const GradArgs& ou
   }
 }
 
+struct TokenInputs {
+  float logit;
+  TokenTerm term;
+};
+
 struct LogprobArgs {
   SliceArgs in;
   const int32_t* tokens;
@@ -282,12 +326,14 @@ struct LogprobArgs {
 // partial set of CTAs in it), by the chain of load, sums, exchange and the row's
 // arithmetic where there are few (64 rows of 248,320: 15 us; 4 of 1,024: 4.3 us).
 template <bool ENT, int THREADS>
-__global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
+    token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int kWarps = THREADS / 32;
   __shared__ float first_max[kWarps];
-  __shared__ float2 warps[kWarps];
+  __shared__ WarpSums warps[kWarps];
   __shared__ CarefulSums careful_warps[kWarps];
   __shared__ PartSlot slots[2][kMaxCluster];
+  __shared__ TokenInputs in;  // warp 0's
   __shared__ int redo;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -302,42 +348,48 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
     return;
   }
   cluster_arrive();  // this CTA runs; waited for before the first access to another's memory
-  const float logit = warp == 0 ? token_logit(a.in, row, token) : 0.0f;
   const int first = min(a.in.units, rank * a.per_part), last = min(a.in.units, first + a.per_part);
   const uint64_t policy = policy_evict_first();
   UnitReader reader(a.in, first, last, threadIdx.x, THREADS);
+  const int own = own_token(token, first, last, threadIdx.x, THREADS);
   float4 v[kBatch];
+  int at = reader.i;
   reader.load(a.in, row, v, policy);
+  swap_token(v, own, at, THREADS, -INFINITY);
+  if (threadIdx.x == 0) in.logit = token_logit(a.in, row, token);
   float m = -FLT_MAX;
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) m = fmaxf(m, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
   m = warp_max(m);
   if (lane == 0) first_max[warp] = m;
   __syncthreads();
-  const float k = fast_reference(warp_max(first_max[lane % kWarps]), a.in.c.c);
+  const float k0 = fast_reference(warp_max(first_max[lane % kWarps]), a.in.c.c);
+  float k = k0;
   FastSums s{};
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+  if (threadIdx.x == 0) in.term = token_term(in.logit, a.in.c);
   while (reader.i < last) {
+    at = reader.i;
     reader.load(a.in, row, v, policy);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+    swap_token(v, own, at, THREADS, -INFINITY);
+    fast_batch<ENT>(s, k, v, a.in.c.c);
   }
-  fast_warp_sums<ENT>(s, warps, warp, lane);
+  fast_warp_sums<ENT>(s, k, k0, warps, warp, lane);
   __syncthreads();
   cluster_wait();  // every CTA of the cluster runs
   if (warp == 0) {
-    const PartStats p = fast_part<ENT, kWarps>(warps, lane, k);
+    const PartStats p = fast_part<ENT, kWarps>(warps, lane);
     if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
   }
   cluster_sync();  // also: no CTA leaves while another may write to it
   if (warp == 0) {
     PartStats p = lane_part(slots[0], lane, a.cluster);
-    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p));
-    p = merge_parts<true, kMaxCluster>(p, a.in.c);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && in.term.holds;
+    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), in.term, in.logit, a.in.c);
     ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
     if (ok && rank == 0) {
-      const RowScore r = row_score<true, ENT>(p, logit, a.in.c);
+      const RowScore r = row_score<true, ENT>(p, in.logit, a.in.c);
       if (lane == 0) {
         a.logprob[row] = static_cast<float>(r.logprob);
         if (ENT) a.entropy[row] = static_cast<float>(r.entropy);
@@ -348,7 +400,7 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
   }
   __syncthreads();
   if (!redo) return;  // the cluster's CTAs agree: they saw the same sums
-  careful_warp_sums(a.in, row, first, last, threadIdx.x, THREADS, careful_warps);
+  careful_warp_sums(a.in, row, token, first, last, threadIdx.x, THREADS, careful_warps);
   __syncthreads();
   if (warp == 0) {
     const PartStats p = careful_part(careful_warps, lane, kWarps, a.in.c);
@@ -356,8 +408,9 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
   }
   cluster_sync();
   if (rank != 0 || warp != 0) return;
-  const PartStats p = merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c);
-  const RowScore r = row_score<false, ENT>(p, logit, a.in.c);
+  const PartStats p =
+      add_token_careful(merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c), in.logit, a.in.c);
+  const RowScore r = row_score<false, ENT>(p, in.logit, a.in.c);
   if (lane == 0) {
     a.logprob[row] = static_cast<float>(r.logprob);
     if (ENT) a.entropy[row] = static_cast<float>(r.entropy);
@@ -392,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_grad_kernel(const 
   if (token >= 0 && token < 4 * a.in.units && (g != 0.0 || h != 0.0)) {
     const float2 s = a.stats[row];
     const double z = fabs(static_cast<double>(s.y)), ent = h != 0.0 ? a.entropy[row] : 0.0f;
-    k = s.y < 0.0f ? grad_coef<false>(g, h, z, log(z), ent, 0.0, s.x, a.in.c, token)
-                   : grad_coef<true>(g, h, z, log(z), ent, 0.0, s.x, a.in.c, token);
+    k = s.y < 0.0f ? grad_coef<false>(g, h, z, log(z), ent, s.x, a.in.c, token)
+                   : grad_coef<true>(g, h, z, log(z), ent, s.x, a.in.c, token);
   }
   part_grad<T, 2>(a.in, a.out, k, row, first, last, threadIdx.x, kThreads);
 }
@@ -419,23 +472,22 @@ struct PolicyArgs {
 // A row's own inputs, read before its sums are ready.
 struct RowInputs {
   float logit, old_logprob, ref_logprob, advantage, weight;
+  TokenTerm term;
 };
-__device__ __forceinline__ RowInputs row_inputs(const PolicyArgs& a, int row, int token) {
-  RowInputs r;
+__device__ __forceinline__ void row_inputs(const PolicyArgs& a, int row, int token, RowInputs& r) {
   // the token's logit, before any CTA may write the gradient over it
   r.logit = token_logit(a.in, row, token);
   r.old_logprob = a.old_logprob[row];
   r.ref_logprob = a.ref_logprob != nullptr ? a.ref_logprob[row] : 0.0f;
   r.advantage = a.advantages[row];
   r.weight = a.weights != nullptr ? a.weights[row] : 1.0f;
-  return r;
 }
 
-// The row's loss and outputs, and the CTA's gradient coefficients, by one warp
-// (every lane holds p, the row's sums; ref is the CTA's reference).
+// The row's loss and outputs, and its gradient coefficients, by one warp (every
+// lane holds p, the row's sums with the token's term).
 template <bool FAST, bool ENT>
 __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int token, const RowInputs& in,
-                                               const PartStats& p, float ref, int lane, bool write) {
+                                               const PartStats& p, int lane, bool write) {
   const RowScore r = row_score<FAST, ENT>(p, in.logit, a.in.c);
   const double w = in.weight, adv = in.advantage;
   const double d = static_cast<double>(in.ref_logprob) - r.logprob;
@@ -465,8 +517,7 @@ __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int
     if (a.kl != nullptr) a.kl[row] = static_cast<float>(kl);
     if (a.entropy != nullptr) a.entropy[row] = static_cast<float>(r.entropy);
   }
-  const double up = FAST ? static_cast<double>(ref) - static_cast<double>(p.ref) : 0.0;
-  return grad_coef<FAST>(w * g, h, r.z, r.log_z, r.entropy, up, FAST ? ref : p.ref, a.in.c, token);
+  return grad_coef<FAST>(w * g, h, r.z, r.log_z, r.entropy, p.ref, a.in.c, token);
 }
 
 // A cluster per row.  KEEP: its threads hold the row in registers between the
@@ -488,9 +539,10 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
   constexpr int kWarps = THREADS / 32;
   __shared__ float first_max[kWarps];
-  __shared__ float2 warps[kWarps];
+  __shared__ WarpSums warps[kWarps];
   __shared__ CarefulSums careful_warps[kWarps];
   __shared__ PartSlot slots[2][kMaxCluster];
+  __shared__ RowInputs in;  // warp 0's
   __shared__ GradCoef coef;
   __shared__ int redo;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -511,49 +563,54 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     return;
   }
   cluster_arrive();  // this CTA runs; waited for before the first access to another's memory
-  RowInputs in{};
-  if (warp == 0) in = row_inputs(a, row, token);
   const uint64_t keep = KEEP ? policy_evict_first() : policy_evict_last();
   UnitReader reader(a.in, first, last, threadIdx.x, THREADS);
+  const int own = own_token(token, first, last, threadIdx.x, THREADS);
   float4 v[kBatch];
+  int at = reader.i;
   reader.load(a.in, row, v, keep);
+  const float own_logit = swap_token(v, own, at, THREADS, -INFINITY);
+  if (threadIdx.x == 0) row_inputs(a, row, token, in);
   float m = -FLT_MAX;
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) m = fmaxf(m, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
   m = warp_max(m);
   if (lane == 0) first_max[warp] = m;
   __syncthreads();
-  const float k = fast_reference(warp_max(first_max[lane % kWarps]), a.in.c.c);
+  const float k0 = fast_reference(warp_max(first_max[lane % kWarps]), a.in.c.c);
+  float k = k0;
   FastSums s{};
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+  if (threadIdx.x == 0) in.term = token_term(in.logit, a.in.c);
   while (!KEEP && reader.i < last) {
+    at = reader.i;
     reader.load(a.in, row, v, keep);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
+    swap_token(v, own, at, THREADS, -INFINITY);
+    fast_batch<ENT>(s, k, v, a.in.c.c);
   }
-  fast_warp_sums<ENT>(s, warps, warp, lane);
+  fast_warp_sums<ENT>(s, k, k0, warps, warp, lane);
   __syncthreads();
   cluster_wait();  // every CTA of the cluster runs
   if (warp == 0) {
-    const PartStats p = fast_part<ENT, kWarps>(warps, lane, k);
+    const PartStats p = fast_part<ENT, kWarps>(warps, lane);
     if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
   }
   cluster_sync();  // also: no CTA leaves while another may write to it
   if (warp == 0) {
     PartStats p = lane_part(slots[0], lane, a.cluster);
-    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p));
-    p = merge_parts<true, kMaxCluster>(p, a.in.c);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && in.term.holds;
+    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), in.term, in.logit, a.in.c);
     ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
     if (ok) {
-      const GradCoef g = policy_row<true, ENT>(a, row, token, in, p, k, lane, rank == 0);
+      const GradCoef g = policy_row<true, ENT>(a, row, token, in, p, lane, rank == 0);
       if (lane == 0) coef = g;
     }
     if (lane == 0) redo = !ok;
   }
   __syncthreads();
   if (redo) {  // the cluster's CTAs agree: they saw the same sums
-    careful_warp_sums(a.in, row, first, last, threadIdx.x, THREADS, careful_warps);
+    careful_warp_sums(a.in, row, token, first, last, threadIdx.x, THREADS, careful_warps);
     __syncthreads();
     if (warp == 0) {
       const PartStats p = careful_part(careful_warps, lane, kWarps, a.in.c);
@@ -561,8 +618,9 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     }
     cluster_sync();
     if (warp == 0) {
-      const PartStats p = merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c);
-      const GradCoef g = policy_row<false, ENT>(a, row, token, in, p, p.ref, lane, rank == 0);
+      const PartStats p =
+          add_token_careful(merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c), in.logit, a.in.c);
+      const GradCoef g = policy_row<false, ENT>(a, row, token, in, p, lane, rank == 0);
       if (lane == 0) coef = g;
     }
     __syncthreads();
@@ -572,15 +630,16 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     const GradCoef g = coef;
     const uint64_t once = policy_evict_first();
     const int i0 = first + static_cast<int>(threadIdx.x);
-    SliceCursor at;
-    at.start(min(i0, a.in.units - 1), a.in.per_slice);
+    SliceCursor to;
+    to.start(min(i0, a.in.units - 1), a.in.per_slice);
+    swap_token(v, own, i0, THREADS, own_logit);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + u * THREADS;
       if (i < last) {
-        store_unit(static_cast<T*>(a.out.grad[at.slice]) + static_cast<size_t>(row) * a.in.V_s + 4 * static_cast<size_t>(at.at),
+        store_unit(static_cast<T*>(a.out.grad[to.slice]) + static_cast<size_t>(row) * a.in.V_s + 4 * static_cast<size_t>(to.at),
                    unit_grad(v[u], g, a.in.c, i), once);
-        if (i + THREADS < last) at.advance(THREADS, a.in.per_slice);
+        if (i + THREADS < last) to.advance(THREADS, a.in.per_slice);
       }
     }
   } else {

@@ -7,16 +7,22 @@
 // from which, for a token t,
 //   log p_t = (l_t - m) / T - log z,     H = log z - w / z.
 //
+// The token's own term is left out of the sums and added to them at the end, in
+// 64 bits: where it is nearly all of z, log p_t is what the others leave, and
+// that keeps its digits.
+//
 // The fast form.  e_j = 2^(c l_j - k) with c = log2(e) / T in float32 and k an
 // integer, so a logit costs one fused multiply-add, one ex2 and one addition
 // (and a bound and another multiply-add for w): no running maximum is kept.
 // k is taken from the largest of the first logits each thread of the CTA
-// reads: near the row's maximum, and the same for the whole CTA, so sums add
-// up as they are; the CTAs' different k are powers of two apart, which costs
-// no rounding.  What it rests on is checked afterwards: a row whose sums left
-// [2^-40, 2^60] (a NaN or +inf logit; none above -inf; logits some 30 T above
-// the first ones read, or all of them some 28 T below 0) or whose k exceeds
-// 2^20 is done again in the careful form.  c's rounding is a temperature off by at
+// reads: near the row's maximum, as a rule.  A thread that meets logits far
+// above it (its next sixteen sum to more than 2^5) renews its k and takes them
+// again: an exponent c l_j - k of up to 40 would have a rounding of up to 2^-19
+// in its exponential, one below 5 has 2^-22 at most.  Different k are powers of
+// two apart, so bringing sums together costs no rounding.  What it rests on is
+// checked afterwards: a row whose sums left [2^-40, 2^60] (a NaN or +inf logit;
+// none above -inf; all of them some 28 T below 0) or whose k exceeds 2^20 is
+// done again in the careful form.  c's rounding is a temperature off by at
 // most 2^-24, used consistently: log p_t moves by at most 2^-24 of its distance
 // from the mean of x.
 //
@@ -59,7 +65,8 @@ inline ExpScale exp_scale(float temperature) {
 // ex2.approx is off by at most 1.43e-7 relative on this part and, over a
 // binade, by -5.16e-8 in the mean (measured on 2^18 arguments in each of 30
 // binades; the errors repeat from one to the next).  A sum of many
-// exponentials keeps the mean error, so it is taken out of z, w and p.
+// exponentials keeps the mean error, so it is taken out of z, w and p (but not of
+// the token's own term, which is exact).
 constexpr double kExpMean = 1.0 + 5.16e-8;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -126,9 +133,9 @@ __device__ __forceinline__ float fast_reference(float top, float c) {
 }
 constexpr float kFastMaxK = 1048576.0f;
 
-// Four logits; their exponentials are returned.
+// Four logits.
 template <bool ENT>
-__device__ __forceinline__ float4 fast_add(FastSums& s, const float4& x, float c, float k) {
+__device__ __forceinline__ void fast_add(FastSums& s, const float4& x, float c, float k) {
   const float2 cc = make_float2(c, c), kk = make_float2(-k, -k);
   float2 y0 = fma2(make_float2(x.x, x.y), cc, kk), y1 = fma2(make_float2(x.z, x.w), cc, kk);
   if (ENT) {  // an exponential of 0 times a bounded exponent is 0
@@ -138,7 +145,45 @@ __device__ __forceinline__ float4 fast_add(FastSums& s, const float4& x, float c
   const float2 e0 = make_float2(exp2_fast(y0.x), exp2_fast(y0.y)), e1 = make_float2(exp2_fast(y1.x), exp2_fast(y1.y));
   s.z = add2(s.z, add2(e0, e1));
   if (ENT) s.w = fma2(e1, y1, fma2(e0, y0, s.w));
-  return make_float4(e0.x, e0.y, e1.x, e1.y);
+}
+
+// A thread's sums brought from k to a larger integer, without rounding (w: but
+// for the product's).
+template <bool ENT>
+__device__ __forceinline__ void fast_rebase(FastSums& s, float k, float to) {
+  const float d = k - to;
+  const float f = d < -126.0f ? 0.0f : __int_as_float((127 + static_cast<int>(d)) << 23);  // 2^d
+  if (ENT) {
+    s.w.x = __fmaf_rn(d, s.z.x, s.w.x) * f;
+    s.w.y = __fmaf_rn(d, s.z.y, s.w.y) * f;
+  }
+  s.z.x *= f;
+  s.z.y *= f;
+}
+
+// 4 N logits.  Sixteen near k sum to 2^4.5 at most (an exponent of 2^(1/2) each);
+// above 2^5 k is renewed from the largest of them and they are taken again.
+constexpr float kFastBatchMost = 32.0f;
+template <bool ENT, int N>
+__device__ __forceinline__ void fast_batch(FastSums& s, float& k, const float4 (&v)[N], float c) {
+  FastSums b{};
+#pragma unroll
+  for (int u = 0; u < N; ++u) fast_add<ENT>(b, v[u], c, k);
+  if (b.z.x + b.z.y > kFastBatchMost) {
+    float top = -FLT_MAX;
+#pragma unroll
+    for (int u = 0; u < N; ++u) top = fmaxf(top, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
+    const float to = rintf(top * c);
+    if (to > k && to <= kFastMaxK) {
+      fast_rebase<ENT>(s, k, to);
+      k = to;
+      b = FastSums{};
+#pragma unroll
+      for (int u = 0; u < N; ++u) fast_add<ENT>(b, v[u], c, k);
+    }
+  }
+  s.z = add2(s.z, b.z);
+  if (ENT) s.w = add2(s.w, b.w);
 }
 
 // ------------------------------------------------------------------ careful form
@@ -231,28 +276,72 @@ __device__ __forceinline__ PartStats merge_parts(PartStats p, const ExpScale& c)
   return p;
 }
 
-// Whether a CTA's fast sums hold (a row's, when its parts' do and it is not
-// below kFastLeast).
+// Whether a CTA's fast sums hold (a row's, when its parts' and its token's do and
+// it is not below kFastLeast).
 __device__ __forceinline__ bool fast_holds(const PartStats& p) { return p.z <= 0x1p60 && fabsf(p.ref) <= kFastMaxK; }
 constexpr double kFastLeast = 0x1p-40;
 
+// The token's own term relative to an integer exponent of 2, in 64 bits (0: its
+// logit is -inf, or so low that the term is nothing beside a row that holds).
+struct TokenTerm {
+  double e;
+  float k;
+  bool holds;
+};
+__device__ __forceinline__ TokenTerm token_term(float logit, const ExpScale& c) {
+  TokenTerm t;
+  t.k = rintf(logit * c.c);
+  t.holds = t.k <= kFastMaxK;  // no for +inf and NaN
+  t.e = 0.0;
+  if (t.holds && t.k >= -kFastMaxK)
+    t.e = exp(static_cast<double>(logit) * c.inv_t_fast - static_cast<double>(t.k) * kLn2);
+  else
+    t.k = -FLT_MAX;
+  return t;
+}
+
+// A row's sums with the token's term among them; the exponentials' mean error is
+// taken out of the others'.
+__device__ __forceinline__ PartStats add_token(PartStats p, const TokenTerm& t, float logit, const ExpScale& c) {
+  const float ref = fmaxf(p.ref, t.k);
+  const double d = static_cast<double>(p.ref) - static_cast<double>(ref), f = kExpMean * exp2_int(d);
+  const double e = t.e * exp2_int(static_cast<double>(t.k) - static_cast<double>(ref));
+  p.w = (p.w + d * kLn2 * p.z) * f;
+  if (e > 0.0) p.w += e * (static_cast<double>(logit) * c.inv_t_fast - static_cast<double>(ref) * kLn2);
+  p.z = p.z * f + e;
+  p.ref = ref;
+  return p;
+}
+__device__ __forceinline__ PartStats add_token_careful(PartStats p, float logit, const ExpScale& c) {
+  const float ref = fmaxf(p.ref, logit);
+  const double d = (static_cast<double>(p.ref) - static_cast<double>(ref)) * c.inv_t;
+  const double x = (static_cast<double>(logit) - static_cast<double>(ref)) * c.inv_t;
+  const double f = d > -1000.0 ? kExpMean * exp(d) : 0.0;
+  const double e = logit < INFINITY ? (x > -1000.0 ? exp(x) : 0.0) : static_cast<double>(NAN);
+  p.w = (p.w + (d > -1000.0 ? d * p.z : 0.0)) * f;
+  if (e > 0.0) p.w += e * x;
+  p.z = p.z * f + e;
+  p.ref = ref;
+  return p;
+}
+
 // A row's results in 64 bits (a difference of two logprobs, a ratio near a
-// border and the KL estimate near 0 all lose digits in 32).
+// border and the KL estimate near 0 all lose digits in 32), from its sums with
+// the token's term.
 struct RowScore {
   double logprob, z, log_z, entropy;
 };
 template <bool FAST, bool ENT>
 __device__ __forceinline__ RowScore row_score(const PartStats& s, float token_logit, const ExpScale& c) {
   RowScore r;
-  // 0: every logit is -inf; NaN: a NaN or +inf logit
-  r.z = s.z > 0.0 ? s.z * kExpMean : static_cast<double>(NAN);
+  r.z = s.z > 0.0 ? s.z : static_cast<double>(NAN);  // 0: every logit is -inf; NaN: a NaN or +inf logit
   r.log_z = log(r.z);
   const double l = token_logit, ref = s.ref;
   const double x = FAST ? l * c.inv_t_fast - ref * kLn2 : (l - ref) * c.inv_t;
   r.logprob = x - r.log_z;
   r.entropy = 0.0;
   if (ENT) {
-    r.entropy = r.log_z - s.w * kExpMean / r.z;  // less the mean of x under p
+    r.entropy = r.log_z - s.w / r.z;  // less the mean of x under p
     if (r.entropy < 0.0) r.entropy = 0.0;
   }
   if (r.logprob > 0.0) r.logprob = 0.0;
