@@ -6,6 +6,11 @@ PyTorch is used for device memory and streams.  The calls that score tokens
 and add adapters marshal in compiled code (``_binding.so``): their kernels take
 a few microseconds at the smallest sizes.  There is no fallback: if a library
 is missing, importing the binding raises.
+
+``stream`` of a call: the torch stream it runs on (None: the current one).  What
+the call allocates comes from that stream's pool, as under
+``torch.cuda.stream(stream)``; that its inputs are ready there, and its outputs
+where they are used next (``wait_stream``, ``record_stream``), is the caller's.
 """
 import ctypes
 import os
@@ -160,16 +165,24 @@ def _on_device(device):
     return torch.cuda.device(device)
 
 
+def _empty(shape, dtype, dev, stream):
+    """A new tensor from the pool of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def tile_stats_shape(R, S, V_s):
     """Shape of the tile statistics of R rows of S slices of V_s logits: [R, S * B, 8],
     B = ceil(V_s / 128) (one record per block of 128 ids; ``include/vsl.h``)."""
     return (R, S * (-(-V_s // 128)), 8)
 
 
-def _stats_tensor(stats, R, S, V_s, dev):
+def _stats_tensor(stats, R, S, V_s, dev, stream):
     shape = tile_stats_shape(R, S, V_s)
     if stats is True:
-        return torch.empty(shape, dtype=torch.float32, device=dev)
+        return _empty(shape, torch.float32, dev, stream)
     if stats.dtype != torch.float32 or tuple(stats.shape) != shape or not stats.is_contiguous() or stats.device != dev:
         raise ValueError(f"tile statistics must be a contiguous fp32 {list(shape)} tensor on {dev}")
     return stats
@@ -183,7 +196,7 @@ def tile_stats(logits_slices, out=None, stream=None):
     for t in logits_slices:
         if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (R, V_s) or t.device != dev:
             raise ValueError("logits slices must be contiguous fp32 [R, V_s] on one device")
-    out = _stats_tensor(True if out is None else out, R, S, V_s, dev)
+    out = _stats_tensor(True if out is None else out, R, S, V_s, dev, stream)
     with _on_device(dev):
         status = lib.vsl_tile_stats(_ptr_array(logits_slices), R, S, V_s, _ptr(out), _stream_handle(stream, dev))
     _check(status, "vsl_tile_stats")
@@ -202,7 +215,7 @@ def logits_local(hidden, w_slices, out=None, stream=None, tile_stats=None):
     S = len(w_slices)
     V_s = w_slices[0].shape[0]
     if out is None:
-        out = [torch.empty(R, V_s, dtype=torch.float32, device=hidden.device) for _ in range(S)]
+        out = [_empty((R, V_s), torch.float32, hidden.device, stream) for _ in range(S)]
     for t in [hidden, *w_slices, *out]:
         if not t.is_contiguous():
             raise ValueError("logits_local needs contiguous tensors")
@@ -211,7 +224,9 @@ def logits_local(hidden, w_slices, out=None, stream=None, tile_stats=None):
     for t in [*w_slices, *out]:
         if t.device != hidden.device:
             raise ValueError("logits_local: every tensor must be on the hidden states' device")
-    stats = None if tile_stats is None or tile_stats is False else _stats_tensor(tile_stats, R, S, V_s, hidden.device)
+    stats = None
+    if tile_stats is not None and tile_stats is not False:
+        stats = _stats_tensor(tile_stats, R, S, V_s, hidden.device, stream)
     with _on_device(hidden.device):
         status = lib.vsl_logits_local_ex(_ptr(hidden), _ptr_array(w_slices), _ptr_array(out), R, H, S, V_s,
                                          _ptr(stats), _stream_handle(stream, hidden.device))
@@ -284,26 +299,26 @@ def sample(logits_slices, params, seed, n_logprobs, out=None, stream=None, kept_
         raise ValueError("params must be a contiguous int32 [R, 5] tensor (make_row_params)")
     if out is None:
         n = max(n_logprobs, 1)
-        out = SampleResult(torch.empty(R, dtype=torch.int32, device=dev),
-                           torch.empty(R, dtype=torch.float32, device=dev),
-                           torch.empty(R, n, dtype=torch.int32, device=dev)[:, :n_logprobs],
-                           torch.empty(R, n, dtype=torch.float32, device=dev)[:, :n_logprobs],
-                           torch.empty(R, dtype=torch.int32, device=dev))
+        out = SampleResult(_empty(R, torch.int32, dev, stream),
+                           _empty(R, torch.float32, dev, stream),
+                           _empty((R, n), torch.int32, dev, stream)[:, :n_logprobs],
+                           _empty((R, n), torch.float32, dev, stream)[:, :n_logprobs],
+                           _empty(R, torch.int32, dev, stream))
     if params.device != dev:
         raise ValueError("params must be on the logits' device")
     kept_theta = kept_theta or processed
     if kept_theta and out.kept_theta is None:
-        out.kept_theta = torch.empty(R, 2, dtype=torch.float32, device=dev)
+        out.kept_theta = _empty((R, 2), torch.float32, dev, stream)
     if processed and out.processed_logprob is None:
         n = max(n_logprobs, 1)
-        out.processed_logprob = torch.empty(R, dtype=torch.float32, device=dev)
-        out.processed_topn_ids = torch.empty(R, n, dtype=torch.int32, device=dev)[:, :n_logprobs]
-        out.processed_topn_logprob = torch.empty(R, n, dtype=torch.float32, device=dev)[:, :n_logprobs]
+        out.processed_logprob = _empty(R, torch.float32, dev, stream)
+        out.processed_topn_ids = _empty((R, n), torch.int32, dev, stream)[:, :n_logprobs]
+        out.processed_topn_logprob = _empty((R, n), torch.float32, dev, stream)[:, :n_logprobs]
     extras = None
     if tile_stats is not None:
         if not isinstance(tile_stats, torch.Tensor):
             raise TypeError("tile_stats must be the statistics tensor of these logits")
-        tile_stats = _stats_tensor(tile_stats, R, S, V_s, dev)
+        tile_stats = _stats_tensor(tile_stats, R, S, V_s, dev, stream)
         extras = _Extras()
         extras.tile_stats = tile_stats.data_ptr()
     if kept_theta:
@@ -319,7 +334,7 @@ def sample(logits_slices, params, seed, n_logprobs, out=None, stream=None, kept_
             extras.processed_topn_logprob = out.processed_topn_logprob.data_ptr()
     ws_bytes = lib.vsl_sample_workspace_bytes(R, S, V_s, n_logprobs)
     with _on_device(dev):
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        ws = _empty(ws_bytes, torch.uint8, dev, stream) if ws_bytes else None
         topn_ids = out.topn_ids if n_logprobs > 0 else None
         topn_lp = out.topn_logprob if n_logprobs > 0 else None
         status = lib.vsl_sample_ex(_ptr_array(logits_slices), R, S, V_s, _ptr(params),
@@ -360,9 +375,9 @@ def verify_drafts(token_ids, draft_ids, token_logprob=None, out=None, stream=Non
                                       or token_logprob.numel() != token_ids.numel() or token_logprob.device != dev):
         raise ValueError("token_logprob must be a contiguous fp32 tensor like token_ids")
     if out is None:
-        out = VerifyResult(torch.empty(requests, dtype=torch.int32, device=dev),
-                           torch.empty(requests, spec + 1, dtype=torch.int32, device=dev),
-                           torch.empty(requests, spec + 1, device=dev) if token_logprob is not None else None)
+        out = VerifyResult(_empty(requests, torch.int32, dev, stream),
+                           _empty((requests, spec + 1), torch.int32, dev, stream),
+                           _empty((requests, spec + 1), torch.float32, dev, stream) if token_logprob is not None else None)
     with _on_device(dev):
         status = lib.vsl_verify_drafts(_ptr(token_ids), _ptr(token_logprob), _ptr(draft_ids) if spec else None,
                                        requests, spec, _ptr(out.out_ids),
@@ -405,7 +420,7 @@ def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, ou
     stats = None
     if tile_stats is not None and tile_stats is not False:
         R, V_s = logits_slices[0].shape
-        stats = _stats_tensor(tile_stats, R, len(logits_slices), V_s, logits_slices[0].device)
+        stats = _stats_tensor(tile_stats, R, len(logits_slices), V_s, logits_slices[0].device, stream)
     out = _binding.adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale, out, stats, workspace,
                                 _handle(stream))
     return out if stats is None else (out, stats)

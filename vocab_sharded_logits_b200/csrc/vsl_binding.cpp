@@ -19,6 +19,7 @@
 #include <cstdarg>
 #include <exception>
 #include <memory>
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -120,13 +121,29 @@ void need_cuda(at::Device d) {
   if (!d.is_cuda()) raise(PyExc_ValueError, "libvsl needs CUDA tensors, got a tensor on %s", d.str().c_str());
 }
 
-// The stream of a call: the given handle, or the device's current stream.
-void* stream_of(PyObject* o, at::Device d) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(d.index()).stream();
-  void* handle = PyLong_AsVoidPtr(o);
-  if (handle == nullptr && PyErr_Occurred()) throw Raised();
-  return handle;
-}
+// The device and stream of a call (the given handle, or the device's current
+// stream), current while the call lasts: what it allocates comes from the pool
+// of the stream that writes it.
+class Launch {
+ public:
+  Launch(PyObject* handle, at::Device d) {
+    if (handle == Py_None) {
+      device_.emplace(d);
+      stream_ = c10::cuda::getCurrentCUDAStream(d.index()).stream();
+      return;
+    }
+    void* at = PyLong_AsVoidPtr(handle);
+    if (at == nullptr && PyErr_Occurred()) throw Raised();
+    stream_ = static_cast<cudaStream_t>(at);
+    on_.emplace(c10::cuda::getStreamFromExternal(stream_, d.index()));
+  }
+  void* stream() const { return stream_; }
+
+ private:
+  std::optional<c10::cuda::CUDAGuard> device_;
+  std::optional<c10::cuda::CUDAStreamGuard> on_;
+  cudaStream_t stream_ = nullptr;
+};
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device d) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(d));
@@ -210,6 +227,7 @@ PyObject* token_logprobs(PyObject* const* a, Py_ssize_t n) {
   const float temperature = static_cast<float>(number(a[2]));
   const bool entropy = PyObject_IsTrue(a[3]) == 1;
   need_cuda(in.device);
+  const Launch launch(a[7], in.device);
   PyObject* out[3] = {a[4], a[5], a[6]};
   at::Tensor fresh[3];
   void* at[3] = {nullptr, nullptr, nullptr};
@@ -224,13 +242,10 @@ PyObject* token_logprobs(PyObject* const* a, Py_ssize_t n) {
       at[i] = fresh[i].data_ptr();
     }
   }
-  {
-    const c10::cuda::CUDAGuard guard(in.device);
-    check_status(vsl_token_logprobs(in.logits(), in.R, in.S, in.V_s, static_cast<const int32_t*>(tokens), temperature,
-                                    static_cast<float*>(at[0]), static_cast<float*>(at[1]), static_cast<float*>(at[2]),
-                                    stream_of(a[7], in.device)),
-                 "vsl_token_logprobs");
-  }
+  check_status(vsl_token_logprobs(in.logits(), in.R, in.S, in.V_s, static_cast<const int32_t*>(tokens), temperature,
+                                  static_cast<float*>(at[0]), static_cast<float*>(at[1]), static_cast<float*>(at[2]),
+                                  launch.stream()),
+               "vsl_token_logprobs");
   PyObject* result = PyTuple_New(3);
   if (result == nullptr) throw Raised();
   for (int i = 0; i < 3; ++i) {
@@ -259,17 +274,14 @@ PyObject* token_logprobs_grad(PyObject* const* a, Py_ssize_t n) {
   const void* entropy =
       d_entropy != nullptr ? address(a[4], "forward.entropy", at::kFloat, {in.R}, in.device) : nullptr;
   need_cuda(in.device);
+  const Launch launch(a[9], in.device);
   OutSlices grad(a[7], "grad", grad_type(a[8]), true, in);
-  {
-    const c10::cuda::CUDAGuard guard(in.device);
-    check_status(
-        vsl_token_logprobs_grad(in.logits(), in.R, in.S, in.V_s, static_cast<const int32_t*>(tokens), temperature,
-                                static_cast<const float*>(stats), static_cast<const float*>(entropy),
-                                static_cast<const float*>(d_logprob), static_cast<const float*>(d_entropy),
-                                grad.at.data(), grad.type == at::kBFloat16 ? VSL_GRAD_BF16 : VSL_GRAD_FP32,
-                                stream_of(a[9], in.device)),
-        "vsl_token_logprobs_grad");
-  }
+  check_status(vsl_token_logprobs_grad(in.logits(), in.R, in.S, in.V_s, static_cast<const int32_t*>(tokens), temperature,
+                                       static_cast<const float*>(stats), static_cast<const float*>(entropy),
+                                       static_cast<const float*>(d_logprob), static_cast<const float*>(d_entropy),
+                                       grad.at.data(), grad.type == at::kBFloat16 ? VSL_GRAD_BF16 : VSL_GRAD_FP32,
+                                       launch.stream()),
+               "vsl_token_logprobs_grad");
   return grad.take();
 }
 
@@ -290,6 +302,7 @@ PyObject* policy_loss(PyObject* const* a, Py_ssize_t n) {
   i.entropy_coef = static_cast<float>(number(a[9]));
   i.temperature = static_cast<float>(number(a[10]));
   need_cuda(in.device);
+  const Launch launch(a[13], in.device);
   const bool with_grad = a[11] != Py_False;
   const at::Tensor rows = empty({4 * static_cast<int64_t>(in.R)}, at::kFloat, in.device);
   float* at = rows.data_ptr<float>();
@@ -306,9 +319,7 @@ PyObject* policy_loss(PyObject* const* a, Py_ssize_t n) {
       o.grad_slices = grad->at.data();
       o.grad_type = grad->type == at::kBFloat16 ? VSL_GRAD_BF16 : VSL_GRAD_FP32;
     }
-    const c10::cuda::CUDAGuard guard(in.device);
-    check_status(vsl_policy_loss(in.logits(), in.R, in.S, in.V_s, &i, &o, stream_of(a[13], in.device)),
-                 "vsl_policy_loss");
+    check_status(vsl_policy_loss(in.logits(), in.R, in.S, in.V_s, &i, &o, launch.stream()), "vsl_policy_loss");
     if (with_grad) grad_list = grad->take();
   }
   PyObject* result = PyTuple_New(5);
@@ -341,16 +352,14 @@ PyObject* preference_loss(PyObject* const* a, Py_ssize_t n) {
   const void* weights = address(a[3], "weights", at::kFloat, {pairs}, device, true);
   const float beta = static_cast<float>(number(a[4])), smoothing = static_cast<float>(number(a[5]));
   need_cuda(device);
+  const Launch launch(a[6], device);
   const at::Tensor loss = empty({pairs}, at::kFloat, device), rewards = empty({pairs, 2}, at::kFloat, device);
   const at::Tensor d = empty({R}, at::kFloat, device);
-  {
-    const c10::cuda::CUDAGuard guard(device);
-    check_status(vsl_preference_loss(static_cast<const float*>(lp), static_cast<const float*>(ref),
-                                     static_cast<const int32_t*>(at), static_cast<const float*>(weights), R, pairs,
-                                     beta, smoothing, loss.data_ptr<float>(), rewards.data_ptr<float>(),
-                                     d.data_ptr<float>(), stream_of(a[6], device)),
-                 "vsl_preference_loss");
-  }
+  check_status(vsl_preference_loss(static_cast<const float*>(lp), static_cast<const float*>(ref),
+                                   static_cast<const int32_t*>(at), static_cast<const float*>(weights), R, pairs, beta,
+                                   smoothing, loss.data_ptr<float>(), rewards.data_ptr<float>(), d.data_ptr<float>(),
+                                   launch.stream()),
+               "vsl_preference_loss");
   PyObject* result = PyTuple_New(3);
   if (result == nullptr) throw Raised();
   PyTuple_SET_ITEM(result, 0, wrap(loss));
@@ -382,31 +391,23 @@ PyObject* adapters_add(PyObject* const* a, Py_ssize_t n) {
   const void* ids = address(a[4], "adapter_ids", at::kInt, {in.R}, in.device);
   const void* scale = address(a[5], "scale", at::kFloat, {adapters}, in.device, true);
   need_cuda(in.device);
+  const Launch launch(a[9], in.device);
   OutSlices out(a[6], "out", at::kFloat, false, in);
   void* stats = a[7] == Py_None ? nullptr
                                 : address(a[7], "tile_stats", at::kFloat,
                                           {in.R, static_cast<int64_t>(in.S) * ((in.V_s + 127) / 128), 8}, in.device);
-  void* stream = stream_of(a[9], in.device);
-  const c10::cuda::CUDAGuard guard(in.device);
   at::Tensor workspace;
   if (a[8] != Py_None) {
     workspace = tensor(a[8], "workspace");
     if (workspace.scalar_type() != at::kByte || !workspace.is_contiguous() || workspace.device() != in.device)
       raise(PyExc_ValueError, "workspace must be a contiguous uint8 tensor on %s", in.device.str().c_str());
   } else {
-    const int64_t bytes = static_cast<int64_t>(vsl_adapters_workspace_bytes(in.R, adapters, rank));
-    if (a[9] == Py_None) {
-      workspace = empty({bytes}, at::kByte, in.device);
-    } else {  // from the pool of the stream that uses it
-      const c10::cuda::CUDAStreamGuard on(
-          c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), in.device.index()));
-      workspace = empty({bytes}, at::kByte, in.device);
-    }
+    workspace = empty({static_cast<int64_t>(vsl_adapters_workspace_bytes(in.R, adapters, rank))}, at::kByte, in.device);
   }
   check_status(vsl_adapters_add(in.logits(), reinterpret_cast<float* const*>(out.at.data()), hidden, in.R, H, in.S,
                                 in.V_s, pool_at, b_at.data(), static_cast<const float*>(scale), adapters, rank,
                                 static_cast<const int32_t*>(ids), static_cast<float*>(stats), workspace.data_ptr(),
-                                static_cast<size_t>(workspace.numel()), stream),
+                                static_cast<size_t>(workspace.numel()), launch.stream()),
                "vsl_adapters_add");
   return out.take();
 }
