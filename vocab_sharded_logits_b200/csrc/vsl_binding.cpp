@@ -72,7 +72,9 @@ void* address(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRe
   return t.data_ptr();
 }
 
-struct Sequence {  // a list or tuple
+// A list or tuple; of any other iterable a list, which alone may hold its
+// tensors: their addresses are good as long as this lives.
+struct Sequence {
   PyObject* fast;
   Py_ssize_t size;
   Sequence(PyObject* o, const char* name) : fast(PySequence_Fast(o, name)) {
@@ -93,12 +95,12 @@ int as_int(int64_t v, const char* name) {
 
 // The logits slices of a call.
 struct Slices {
+  Sequence list;
   Addresses at;
   int R = 0, S = 0, V_s = 0;
   at::Device device = at::Device(at::kCPU);
 
-  Slices(PyObject* o, const char* where) {
-    Sequence list(o, "logits_slices must be a list of tensors");
+  Slices(PyObject* o, const char* where) : list(o, "logits_slices must be a list of tensors") {
     if (list.size == 0) raise(PyExc_ValueError, "%s: no logits slices", where);
     const at::Tensor& first = tensor(list[0], "logits_slices");
     if (first.dim() != 2) raise(PyExc_ValueError, "%s: logits slices must be [R, V_s]", where);
@@ -188,7 +190,7 @@ struct OutSlices {
         if (type != at::kFloat && type != at::kBFloat16) raise(PyExc_TypeError, "the gradient is float32 or bfloat16");
       }
       for (int s = 0; s < in.S; ++s) at.push_back(address(l[s], name, type, {in.R, in.V_s}, in.device));
-      list = given;
+      list = l.fast;
       Py_INCREF(list);
       return;
     }
