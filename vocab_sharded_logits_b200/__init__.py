@@ -4,8 +4,9 @@ A thin binding over the C ABI of ``libvsl.so`` (``include/vsl.h``): argument
 marshalling only; every step of the path runs in the library's CUDA kernels.
 PyTorch is used for device memory and streams.  The calls that score tokens
 and add adapters marshal in compiled code (``_binding.so``): their kernels take
-a few microseconds at the smallest sizes.  There is no fallback: if a library
-is missing, importing the binding raises.
+a few microseconds at the smallest sizes.  There is no fallback: without
+``libvsl.so`` importing raises, without a ``_binding.so`` of this torch and
+Python those calls do.
 
 ``stream`` of a call: the torch stream it runs on (None: the current one).  What
 the call allocates comes from that stream's pool, as under
@@ -128,9 +129,23 @@ def _load():
 
 lib = _load()
 
-from . import _binding  # noqa: E402  (after the library it calls)
 
-_binding.set_error_class(VslError)
+class _MissingBinding:
+    """Stands for a _binding.so that does not load here: each call that needs it raises, the others work."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs {os.path.join(_PKG_DIR, '_binding.so')}, which does not load ({self._why}); "
+                          "build it with vocab_sharded_logits_b200.build")
+
+
+try:
+    from . import _binding  # noqa: E402  (after the library it calls)
+    _binding.set_error_class(VslError)
+except ImportError as _error:  # built for another torch or Python
+    _binding = _MissingBinding(str(_error))
 
 
 def status_string(status):
