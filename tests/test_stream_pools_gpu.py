@@ -40,6 +40,7 @@ def _calls(dev):
     b = [rand(n, V_s, rank).bfloat16() for _ in range(S)]
     ids = torch.tensor([0, 1, -1, 0, 1, 1], dtype=torch.int32, device=dev)
     tok, one = torch.arange(R, dtype=torch.int32, device=dev), torch.ones(R, device=dev)
+    old = -one                      # made here: a call under another stream would not wait for it
     at = torch.tensor([0, 3, R], dtype=torch.int32, device=dev)
     params = vsl.make_row_params(np.ones(R), np.full(R, 40), np.ones(R), np.arange(R), np.zeros(R), dev)
     fwd = vsl.token_logprobs(logits, tok, entropy=True)
@@ -53,7 +54,7 @@ def _calls(dev):
         "adapters_add": lambda **k: vsl.adapters_add(logits, hidden, a, b, ids, tile_stats=True, **k),
         "token_logprobs": lambda **k: vsl.token_logprobs(logits, tok, entropy=True, **k),
         "token_logprobs_grad": lambda **k: vsl.token_logprobs_grad(logits, tok, fwd, one, one, **k),
-        "policy_loss": lambda **k: vsl.policy_loss(logits, tok, -one, one, entropy_coef=0.1, **k),
+        "policy_loss": lambda **k: vsl.policy_loss(logits, tok, old, one, entropy_coef=0.1, **k),
         "preference_loss": lambda **k: vsl.preference_loss(one, None, at, 0.1, **k),
     }
 
