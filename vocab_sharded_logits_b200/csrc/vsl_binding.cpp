@@ -167,6 +167,12 @@ PyObject* wrap(const at::Tensor& t) {
   return o;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();
+  return v == 1;
+}
+
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Raised();
@@ -227,7 +233,7 @@ PyObject* token_logprobs(PyObject* const* a, Py_ssize_t n) {
   const Slices in(a[0], "token_logprobs");
   const void* tokens = address(a[1], "token_ids", at::kInt, {in.R}, in.device);
   const float temperature = static_cast<float>(number(a[2]));
-  const bool entropy = PyObject_IsTrue(a[3]) == 1;
+  const bool entropy = truth(a[3]);
   need_cuda(in.device);
   const Launch launch(a[7], in.device);
   PyObject* out[3] = {a[4], a[5], a[6]};
@@ -261,7 +267,7 @@ PyObject* token_logprobs(PyObject* const* a, Py_ssize_t n) {
   return result;
 }
 
-at::ScalarType grad_type(PyObject* bf16) { return PyObject_IsTrue(bf16) == 1 ? at::kBFloat16 : at::kFloat; }
+at::ScalarType grad_type(PyObject* bf16) { return truth(bf16) ? at::kBFloat16 : at::kFloat; }
 
 // token_logprobs_grad(slices, token_ids, temperature, row_stats, entropy, d_logprob, d_entropy, grad, bf16, stream)
 PyObject* token_logprobs_grad(PyObject* const* a, Py_ssize_t n) {
