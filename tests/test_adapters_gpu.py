@@ -313,3 +313,22 @@ def test_small_terms_survive_a_cancelled_logit_above_rank_64(cuda_device, rank):
         ids = torch.zeros(R, dtype=torch.int32, device=cuda_device)
         out, = vsl.adapters_add([logits], bf16(hidden), bf16(a), [bf16(b)], ids)
         assert bool((out == 2.0 ** -10 + 2.0 ** -17 + 2.0 ** -20 + 2.0 ** -27).all())
+
+
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("per", [1, 2, 3, 20])
+def test_a_finite_product_at_the_end_of_the_range(cuda_device, rank, per):
+    """u = +-(2^128 - 2^118), finite in float32 and above the largest bf16: its terms are finite too.  B = 2^-120 gives
+    +-255.75 exactly, B = 0 nothing, however many rows share the adapter."""
+    R, H, V_s = 2 * per, 16, 260
+    hidden = torch.zeros(R, H)
+    hidden[:, :10] = 2.0 ** torch.arange(127.0, 117.0, -1.0)
+    hidden[per:] *= -1
+    a, b = torch.zeros(2, rank, H), torch.zeros(2, V_s, rank)
+    a[:, rank - 1], b[:, ::2, rank - 1] = 1.0, 2.0 ** -120
+    bf16 = lambda x: x.to(cuda_device, torch.bfloat16)  # noqa: E731
+    logits = torch.ones(R, V_s, device=cuda_device)
+    ids = (torch.arange(R, device=cuda_device) // per).int()
+    out, = vsl.adapters_add([logits], bf16(hidden), bf16(a), [bf16(b)], ids)
+    assert bool((out[:, 1::2] == 1).all())
+    assert bool((out[:per, ::2] == 256.75).all()) and bool((out[per:, ::2] == -254.75).all())

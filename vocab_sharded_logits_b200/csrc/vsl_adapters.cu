@@ -14,7 +14,7 @@
 // share one adapter, so no row ever meets another adapter's numbers: one
 // request's infinities or NaNs never reach another's row, and no product is
 // computed to be thrown away.  u is not rounded to bf16: it is carried as three
-// bf16 terms (8 + 8 + 8 bits), each multiplied with B.
+// bf16 terms (8 + 8 + 8 bits, cut off one after another), each multiplied with B.
 //
 // What it cannot do without: one read and one write of the logits and one read
 // of each used adapter's A and B.  Measured (H = 4,096 but where stated, of the
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
                          2 * (4 * (4 * (r & 7) + quad) + reg) + (rank & 1);
 #pragma unroll
     for (int i = 0; i < kTerms; ++i) {
-      const __nv_bfloat16 term = __float2bfloat16_rn(u);
+      const __nv_bfloat16 term = __float2bfloat16_rz(u);  // cut off: of a finite u never infinite
       out[2 * i * kFragment] = term;
       const float v = __bfloat162float(term);
       u = isfinite(v) ? u - v : 0.0f;  // exact
