@@ -458,15 +458,16 @@ def token_logprobs(logits_slices, token_ids, temperature=1.0, entropy=False, out
 
     logits_slices: list of fp32 [R, V_s] CUDA tensors; token_ids: int32 [R] (outside the vocabulary,
     -1 by convention: the row does not count, its outputs are 0).  out: a ``TokenLogprobs`` to fill
-    again (its entropy too, where it holds one).
+    again (its entropy too, where it holds one; a logprob or row_stats that is None is made).
     """
     if out is None:
         return TokenLogprobs(*_binding.token_logprobs(logits_slices, token_ids, temperature, entropy, None, None, None,
                                                       _handle(stream)), float(temperature))
     if entropy and out.entropy is None:
         raise ValueError("out.entropy is missing")
-    _binding.token_logprobs(logits_slices, token_ids, temperature, out.entropy is not None, out.logprob, out.entropy, out.row_stats,
-                            _handle(stream))
+    out.logprob, out.entropy, out.row_stats = _binding.token_logprobs(
+        logits_slices, token_ids, temperature, out.entropy is not None, out.logprob, out.entropy, out.row_stats,
+        _handle(stream))
     out.temperature = float(temperature)
     return out
 
