@@ -332,3 +332,41 @@ def test_a_finite_product_at_the_end_of_the_range(cuda_device, rank, per):
     out, = vsl.adapters_add([logits], bf16(hidden), bf16(a), [bf16(b)], ids)
     assert bool((out[:, 1::2] == 1).all())
     assert bool((out[:per, ::2] == 256.75).all()) and bool((out[per:, ::2] == -254.75).all())
+
+
+def _unit_sums(a, b, ids, hidden, logits):
+    """The formula in float64 (products of these bf16 values are exact in it): infinities and NaNs as they come."""
+    out = [_np(x) for x in logits]
+    with np.errstate(all="ignore"):
+        for r, i in enumerate(ids):
+            u = (_np(a[i]) * _np(hidden[r])).sum(1)
+            for x, y in zip(out, b):
+                x[r] += (_np(y[i]) * u).sum(1)
+    return out
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 40, 64, 72, 200])
+@pytest.mark.parametrize("per", [1, 2, 3, 20])
+def test_infinite_factors_of_a_rows_own(cuda_device, rank, per):
+    """An infinity in a row's own factors gives what the formula gives, +inf, -inf or NaN, however many rows share the
+    adapter and whatever the rank is padded to."""
+    R, H, V_s = 5 * per, 16, 260
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(rank + per)
+    hidden, logits, a, b, scale, ids = _inputs(R, H, 2, V_s, 5, rank, 3, cuda_device, np.arange(R) // per)
+    inf = float("inf")
+    b[0][0, 3, rank - 1], b[0][0, 5, 0], b[1][0, V_s - 1, 2], b[1][0, 7, :2] = inf, -inf, inf, torch.tensor([inf, -inf])
+    hidden[per:2 * per, 0] = inf                 # u infinite: of one sign in every rank, then of both
+    a[1, :, 0] = a[1, :, 0].abs() + 1
+    b[0][1] = b[0][1].abs() + 1
+    hidden[2 * per:3 * per, 2] = -inf
+    a[3] = 0.0                                   # u = 1 exactly: its small terms are 0
+    a[3, :, 1], hidden[3 * per:4 * per, 1] = 1.0, 1.0
+    b[0][3, 11], b[1][3, 12, rank // 2] = inf, -inf
+    hidden[4 * per:, 3], b[0][4, 9, 1] = inf, inf
+    got = vsl.adapters_add(logits, hidden, a, b, ids)
+    want = _unit_sums(a, b, ids.cpu().numpy(), hidden, logits)
+    for x, y in zip(got, want):
+        x = _np(x)
+        assert np.array_equal(np.isnan(x), np.isnan(y))
+        assert np.array_equal(np.isposinf(x), np.isposinf(y)) and np.array_equal(np.isneginf(x), np.isneginf(y))

@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(cons
     float u = (&parts[0][0][0])[e];
     for (int c = 1; c < p.split; ++c) u += (&parts[c][0][0])[e];
     if (p.scale != nullptr) u *= p.scale[adapter];
+    if (rank >= p.rank) u = 0.0f;  // padding: an infinite hidden state or scale times its zeros is no number
     if (count <= few_rows_of(p.rank)) {  // kept as it is, [row][padded rank]
       if (r < count) reinterpret_cast<float*>(unit_u)[r * steps * 16 + rank] = u;
       continue;
@@ -571,16 +573,16 @@ __device__ __forceinline__ WarpUnit warp_unit(const ExpandArgs& p, int warp, int
 }
 
 // A step's products of 32 ids: y, a lane's B of the four products; a, u's
-// operands of the step; FIRST: the sums begin with it.  ACC = 2: the large
-// term's sums and the two small ones' apart.
-template <bool FIRST, int ACC>
-__device__ __forceinline__ void step_products(float (&d)[ACC][4][4], const uint4 (&a)[kTerms], const uint2 (&y)[4]) {
+// operands of the step; FIRST: the sums begin with it.  The large term's sums and
+// the two small ones' apart.
+template <bool FIRST>
+__device__ __forceinline__ void step_products(float (&d)[2][4][4], const uint4 (&a)[kTerms], const uint2 (&y)[4]) {
 #pragma unroll
   for (int e = 0; e < kTerms; ++e)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float(&to)[4] = d[e == 0 ? 0 : ACC - 1][i];
-      if (FIRST && e < ACC)
+      float(&to)[4] = d[e == 0 ? 0 : 1][i];
+      if (FIRST && e < 2)
         mma_16816_first(to, a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
       else
         mma_16816(to, a[e].x, a[e].y, a[e].z, a[e].w, y[i].x, y[i].y);
@@ -588,20 +590,21 @@ __device__ __forceinline__ void step_products(float (&d)[ACC][4][4], const uint4
 }
 
 // The sums of 32 ids onto the rows' logits, the large terms' first: where those
-// cancel the logit the sum is exact, and the small terms are what is left.
-template <int ACC>
-__device__ __forceinline__ void add_sums(float4 (&x)[2][2], const float (&d)[ACC][4][4]) {
+// cancel the logit the sum is exact, and the small terms are what is left.  An
+// infinity in B times a small term of 0 makes the small terms' sum a NaN, which
+// says nothing: the large ones' is what it should be, and a number is added.
+// (Terms of a u have one sign, so an infinite sum of small ones agrees.)
+__device__ __forceinline__ float small_sum(float d) { return fmaxf(d, -FLT_MAX); }
+__device__ __forceinline__ void add_sums(float4 (&x)[2][2], const float (&d)[2][4][4]) {
 #pragma unroll
-  for (int e = 0; e < ACC; ++e)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        x[i][b].x += d[e][2 * b][2 * i];
-        x[i][b].y += d[e][2 * b][2 * i + 1];
-        x[i][b].z += d[e][2 * b + 1][2 * i];
-        x[i][b].w += d[e][2 * b + 1][2 * i + 1];
-      }
+    for (int b = 0; b < 2; ++b) {
+      x[i][b].x = (x[i][b].x + d[0][2 * b][2 * i]) + small_sum(d[1][2 * b][2 * i]);
+      x[i][b].y = (x[i][b].y + d[0][2 * b][2 * i + 1]) + small_sum(d[1][2 * b][2 * i + 1]);
+      x[i][b].z = (x[i][b].z + d[0][2 * b + 1][2 * i]) + small_sum(d[1][2 * b + 1][2 * i]);
+      x[i][b].w = (x[i][b].w + d[0][2 * b + 1][2 * i + 1]) + small_sum(d[1][2 * b + 1][2 * i + 1]);
+    }
 }
 
 // Stores a quarter of the unit's rows, j its first id; a lane's logits past the
