@@ -107,16 +107,16 @@ __device__ __forceinline__ void fast_warp_sums(FastSums s, float k, float k0, Wa
 template <bool ENT, int WARPS>
 __device__ __forceinline__ PartStats fast_part(const WarpSums* shared, int lane) {
   static_assert(WARPS <= 16, "lanes 0 .. 15 hold the result");
-  PartStats p{0.0, 0.0, -FLT_MAX};
+  PartStats p{0.0, 0.0, shared[0].k};
   if (lane < WARPS) {
     p.z = shared[lane].z;
     p.w = shared[lane].w;
     p.ref = shared[lane].k;
   }
-  float ref = p.ref;
+  if (!__all_sync(0xFFFFFFFFu, p.ref == shared[0].k)) {  // rare: a warp renewed its k
+    float ref = p.ref;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
-  if (p.ref != ref) {
+    for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xFFFFFFFFu, ref, o));
     const double d = fmax(static_cast<double>(p.ref) - static_cast<double>(ref), -2000.0), f = exp2_int(d);
     p.w = (p.w + d * p.z) * f;
     p.z *= f;
@@ -305,11 +305,6 @@ __device__ __forceinline__ void part_grad(const SliceArgs& a, const GradArgs& ou
   }
 }
 
-struct TokenInputs {
-  float logit;
-  TokenTerm term;
-};
-
 struct LogprobArgs {
   SliceArgs in;
   const int32_t* tokens;
@@ -333,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   __shared__ WarpSums warps[kWarps];
   __shared__ CarefulSums careful_warps[kWarps];
   __shared__ PartSlot slots[2][kMaxCluster];
-  __shared__ TokenInputs in;  // warp 0's
+  __shared__ float logit;  // the token's
   __shared__ int redo;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -356,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   int at = reader.i;
   reader.load(a.in, row, v, policy);
   swap_token(v, own, at, THREADS, -INFINITY);
-  if (threadIdx.x == 0) in.logit = token_logit(a.in, row, token);
+  if (threadIdx.x == 0) logit = token_logit(a.in, row, token);
   float m = -FLT_MAX;
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) m = fmaxf(m, fmaxf(fmaxf(v[u].x, v[u].y), fmaxf(v[u].z, v[u].w)));
@@ -368,7 +363,6 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   FastSums s{};
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
-  if (threadIdx.x == 0) in.term = token_term(in.logit, a.in.c);
   while (reader.i < last) {
     at = reader.i;
     reader.load(a.in, row, v, policy);
@@ -382,14 +376,17 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
     const PartStats p = fast_part<ENT, kWarps>(warps, lane);
     if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
   }
-  cluster_sync();  // also: no CTA leaves while another may write to it
+  cluster_arrive();
+  TokenTerm term{};
+  if (warp == 0) term = token_term(logit, a.in.c);  // while the sums travel
+  cluster_wait();  // also: no CTA leaves while another may write to it
   if (warp == 0) {
     PartStats p = lane_part(slots[0], lane, a.cluster);
-    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && in.term.holds;
-    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), in.term, in.logit, a.in.c);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && term.holds;
+    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), term, logit, a.in.c);
     ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
     if (ok && rank == 0) {
-      const RowScore r = row_score<true, ENT>(p, in.logit, a.in.c);
+      const RowScore r = row_score<true, ENT>(p, logit, a.in.c);
       if (lane == 0) {
         a.logprob[row] = static_cast<float>(r.logprob);
         if (ENT) a.entropy[row] = static_cast<float>(r.entropy);
@@ -409,8 +406,8 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   cluster_sync();
   if (rank != 0 || warp != 0) return;
   const PartStats p =
-      add_token_careful(merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c), in.logit, a.in.c);
-  const RowScore r = row_score<false, ENT>(p, in.logit, a.in.c);
+      add_token_careful(merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c), logit, a.in.c);
+  const RowScore r = row_score<false, ENT>(p, logit, a.in.c);
   if (lane == 0) {
     a.logprob[row] = static_cast<float>(r.logprob);
     if (ENT) a.entropy[row] = static_cast<float>(r.entropy);
@@ -472,7 +469,6 @@ struct PolicyArgs {
 // A row's own inputs, read before its sums are ready.
 struct RowInputs {
   float logit, old_logprob, ref_logprob, advantage, weight;
-  TokenTerm term;
 };
 __device__ __forceinline__ void row_inputs(const PolicyArgs& a, int row, int token, RowInputs& r) {
   // the token's logit, before any CTA may write the gradient over it
@@ -582,7 +578,6 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
   FastSums s{};
 #pragma unroll
   for (int u = 0; u < kBatch; ++u) fast_add<ENT>(s, v[u], a.in.c.c, k);
-  if (threadIdx.x == 0) in.term = token_term(in.logit, a.in.c);
   while (!KEEP && reader.i < last) {
     at = reader.i;
     reader.load(a.in, row, v, keep);
@@ -596,11 +591,14 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     const PartStats p = fast_part<ENT, kWarps>(warps, lane);
     if (lane < a.cluster) send_part(&slots[0][rank], lane, p);
   }
-  cluster_sync();  // also: no CTA leaves while another may write to it
+  cluster_arrive();
+  TokenTerm term{};
+  if (warp == 0) term = token_term(in.logit, a.in.c);  // while the sums travel
+  cluster_wait();  // also: no CTA leaves while another may write to it
   if (warp == 0) {
     PartStats p = lane_part(slots[0], lane, a.cluster);
-    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && in.term.holds;
-    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), in.term, in.logit, a.in.c);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && term.holds;
+    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), term, in.logit, a.in.c);
     ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
     if (ok) {
       const GradCoef g = policy_row<true, ENT>(a, row, token, in, p, lane, rank == 0);
