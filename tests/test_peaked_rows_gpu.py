@@ -131,3 +131,38 @@ def test_the_tokens_own_term_alone(cuda_device):
         assert np.isnan(_np(got.logprob)[6:]).all() and np.isnan(_np(got.entropy)[6:]).all()
     # 1 - p_token: the exponential's, z's and the coefficient's roundings
     assert (np.abs(grad[:6]) <= 2.0 ** -22 + 2.0 ** -21).all() and np.isnan(grad[6:]).all()
+
+
+@pytest.mark.parametrize("height", [3.0, 10.0, 18.0, 28.0])
+@pytest.mark.parametrize("ent_coef", [0.0, 0.02])
+@pytest.mark.parametrize("V,S", SIZES)
+def test_the_gradient_at_a_token_on_top(cuda_device, V, S, ent_coef, height):
+    """(g (1 - p) - h p (log p + H)) / T at the token.  The policy loss has the row's sums in 64 bits: 1 - p is what the
+    rest leaves, not a difference of two numbers near 1.  The logprobs' gradient gets z and the entropy in 32 and takes
+    the difference: p's exponential (2^-22 and its mean error), its exponent below 1/2 and the steps of z, the
+    coefficients, their product and the difference."""
+    l, top = _rows(V, height, 3, (0.3, 0.9999))
+    rows = np.arange(16)
+    logp = O.log_softmax(l)
+    lp, ent = O.token_logprobs(l, top)
+    p, dist = np.exp(logp), logp[rows, top][:, None] - logp
+    p[rows, top] = 0.0
+    rest, near = p.sum(1), np.where(p > 2.0 ** -60, dist, 0.0).max(1)
+    eps, size = _rest_error(V, near), (p * (2 * dist + 34)).sum(1)
+    slices, tok = _slices(l, S, cuda_device), torch.from_numpy(top).to(cuda_device)
+    old = np.zeros(16, np.float32)
+    want = O.policy_loss(l, top, old, -np.ones(16), ent_coef=np.float64(np.float32(ent_coef)))
+    one = torch.ones(16, device=cuda_device)
+    pol = vsl.policy_loss(slices, tok, 0 * one, -one, entropy_coef=ent_coef)
+    got = np.concatenate([_np(x) for x in pol.grad], 1)[rows, top]
+    exact = want["grad"][rows, top]
+    # ratio exp(log p - old) moves with log p, by rest * eps; 1 - p, log p and H by the same and by size * eps
+    bound = 2 * rest * eps + ent_coef * (rest + size) * eps + STEP * np.abs(exact) + 2.0 ** -48
+    assert (np.abs(got - exact) <= bound).all(), (np.abs(got - exact) / bound).max()
+    fwd = vsl.token_logprobs(slices, tok, entropy=True)
+    h = np.full(16, ent_coef, np.float32)
+    grad = vsl.token_logprobs_grad(slices, tok, fwd, one, _dev(h, cuda_device) if ent_coef else None)
+    exact = O.token_logprobs_grad(l, top, np.ones(16), h.astype(np.float64))[rows, top]
+    off = np.abs(np.concatenate([_np(x) for x in grad], 1)[rows, top] - exact)
+    bound = (1 + 2 * ent_coef) * (2.0 ** -22 + 6 * STEP) + rest * eps + ent_coef * ((rest + size) * eps + STEP * ent)
+    assert (off <= bound).all(), (off / bound).max()

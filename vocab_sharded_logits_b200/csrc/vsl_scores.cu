@@ -73,21 +73,18 @@ __device__ __forceinline__ int own_token(int token, int first, int last, int thr
   const int u = token >> 2;
   return u >= first && u < last && ((u - first) & (threads - 1)) == thread ? token : -1;
 }
-// Puts `value` in the own token's place in the batch whose first unit is i;
-// returns what stood there.
-__device__ __forceinline__ float swap_token(float4 (&v)[kBatch], int own, int i, int step, float value) {
-  float old = value;
+// Leaves the own token out of the batch whose first unit is i.
+__device__ __forceinline__ void drop_token(float4 (&v)[kBatch], int own, int i, int step) {
   const int unit = own >> 2;
   if (unit >= i && unit < i + kBatch * step) {  // rare; never for -1
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       if (unit == i + u * step) {
         const int j = own & 3;
-        old = j == 0 ? v[u].x : j == 1 ? v[u].y : j == 2 ? v[u].z : v[u].w;
-        v[u] = make_float4(j == 0 ? value : v[u].x, j == 1 ? value : v[u].y, j == 2 ? value : v[u].z, j == 3 ? value : v[u].w);
+        v[u] = make_float4(j == 0 ? -INFINITY : v[u].x, j == 1 ? -INFINITY : v[u].y, j == 2 ? -INFINITY : v[u].z,
+                           j == 3 ? -INFINITY : v[u].w);
       }
   }
-  return old;
 }
 
 // A CTA's threads bring their sums together: each warp's into shared memory,
@@ -143,7 +140,7 @@ __device__ __noinline__ void careful_warp_sums(const SliceArgs& a, int row, int 
     float4 v[kBatch];
     const int i = reader.i;
     reader.load(a, row, v, policy);
-    swap_token(v, own, i, threads, -INFINITY);
+    drop_token(v, own, i, threads);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) careful_add(s, v[u], a.c);
   }
@@ -200,8 +197,9 @@ __device__ __forceinline__ void store_unit(__nv_bfloat16* p, const float4& g, ui
 }
 
 // A row's gradient coefficients (see the file's head): G_j = e_j (alpha + gamma
-// y_j) + at_token 1[j = token], where y_j is what e_j is taken from: the exponent
-// c l_j - ref of 2 (fast), or l_j - ref (careful).
+// y_j), where y_j is what e_j is taken from: the exponent c l_j - ref of 2
+// (fast), or l_j - ref (careful).  at_token: what comes to it at the token, or,
+// where the row's sums are at hand in 64 bits (token_grad), its value.
 struct GradCoef {
   float ref, alpha, gamma, at_token;
   int token;  // -1: the row does not count, its gradient is 0
@@ -223,21 +221,33 @@ __device__ __forceinline__ GradCoef grad_coef(double g, double h, double z, doub
   return k;
 }
 
+// The gradient at the token, in 64 bits: 1 - p (`rest`) of a token that is nearly
+// certain is no difference of two numbers near 1.
+__device__ __forceinline__ float token_grad(double g, double h, double logprob, double rest, double entropy,
+                                            const ExpScale& c) {
+  double v = g * rest;
+  if (h != 0.0 && rest != 1.0) v -= h * (1.0 - rest) * (logprob + entropy);
+  return static_cast<float>(v * c.inv_t);
+}
+
 struct GradArgs {
   void* grad[VSL_MAX_SLICES];
 };
 
-__device__ __forceinline__ void add_at_token(const GradCoef& k, int i, float4& g) {
+// What at_token is to the gradient at the token: its value, or what is added.
+template <bool SET>
+__device__ __forceinline__ void at_the_token(const GradCoef& k, int i, float4& g) {
   const int at = k.token - 4 * i;
   if (at >= 0 && at < 4) {
-    if (at == 0) g.x += k.at_token;
-    if (at == 1) g.y += k.at_token;
-    if (at == 2) g.z += k.at_token;
-    if (at == 3) g.w += k.at_token;
+    if (at == 0) g.x = SET ? k.at_token : g.x + k.at_token;
+    if (at == 1) g.y = SET ? k.at_token : g.y + k.at_token;
+    if (at == 2) g.z = SET ? k.at_token : g.z + k.at_token;
+    if (at == 3) g.w = SET ? k.at_token : g.w + k.at_token;
   }
 }
 
 // Gradient of one unit (the i-th of the row) from its logits.
+template <bool SET>
 __device__ __forceinline__ float4 unit_grad(const float4& x, const GradCoef& k, const ExpScale& c, int i) {
   const float v[4] = {x.x, x.y, x.z, x.w};
   float g[4];
@@ -264,13 +274,13 @@ __device__ __forceinline__ float4 unit_grad(const float4& x, const GradCoef& k, 
     }
   }
   float4 r = make_float4(g[0], g[1], g[2], g[3]);
-  add_at_token(k, i, r);
+  at_the_token<SET>(k, i, r);
   return r;
 }
 
 // Gradient of units [first, last) of a row from global memory, a slice's run
 // at a time.
-template <typename T, int BATCH = kBatch>
+template <typename T, bool SET, int BATCH = kBatch>
 __device__ __forceinline__ void part_grad(const SliceArgs& a, const GradArgs& out, const GradCoef& k, int row,
                                           int first, int last, int thread, int threads) {
   SliceCursor run;
@@ -290,7 +300,7 @@ __device__ __forceinline__ void part_grad(const SliceArgs& a, const GradArgs& ou
           if (i + b * threads < n) x[b] = ldg_hint4(src + 4 * (i + b * threads), once);
 #pragma unroll
         for (int b = 0; b < BATCH; ++b)
-          if (i + b * threads < n) x[b] = unit_grad(x[b], k, a.c, u + i + b * threads);
+          if (i + b * threads < n) x[b] = unit_grad<SET>(x[b], k, a.c, u + i + b * threads);
       } else {
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) x[b] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   float4 v[kBatch];
   int at = reader.i;
   reader.load(a.in, row, v, policy);
-  swap_token(v, own, at, THREADS, -INFINITY);
+  drop_token(v, own, at, THREADS);
   if (threadIdx.x == 0) logit = token_logit(a.in, row, token);
   float m = -FLT_MAX;
 #pragma unroll
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   while (reader.i < last) {
     at = reader.i;
     reader.load(a.in, row, v, policy);
-    swap_token(v, own, at, THREADS, -INFINITY);
+    drop_token(v, own, at, THREADS);
     fast_batch<ENT>(s, k, v, a.in.c.c);
   }
   fast_warp_sums<ENT>(s, k, k0, warps, warp, lane);
@@ -381,9 +391,9 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   if (warp == 0) term = token_term(logit, a.in.c);  // while the sums travel
   cluster_wait();  // also: no CTA leaves while another may write to it
   if (warp == 0) {
-    PartStats p = lane_part(slots[0], lane, a.cluster);
-    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && term.holds;
-    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), term, logit, a.in.c);
+    const PartStats part = lane_part(slots[0], lane, a.cluster);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(part)) && term.holds;
+    const RowStats p = add_token(merge_parts<true, kMaxCluster>(part, a.in.c), term, logit, a.in.c);
     ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
     if (ok && rank == 0) {
       const RowScore r = row_score<true, ENT>(p, logit, a.in.c);
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
   }
   cluster_sync();
   if (rank != 0 || warp != 0) return;
-  const PartStats p =
+  const RowStats p =
       add_token_careful(merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c), logit, a.in.c);
   const RowScore r = row_score<false, ENT>(p, logit, a.in.c);
   if (lane == 0) {
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_logprobs_grad_kernel(const 
     k = s.y < 0.0f ? grad_coef<false>(g, h, z, log(z), ent, s.x, a.in.c, token)
                    : grad_coef<true>(g, h, z, log(z), ent, s.x, a.in.c, token);
   }
-  part_grad<T, 2>(a.in, a.out, k, row, first, last, threadIdx.x, kThreads);
+  part_grad<T, false, 2>(a.in, a.out, k, row, first, last, threadIdx.x, kThreads);
 }
 
 struct PolicyArgs {
@@ -483,7 +493,7 @@ __device__ __forceinline__ void row_inputs(const PolicyArgs& a, int row, int tok
 // lane holds p, the row's sums with the token's term).
 template <bool FAST, bool ENT>
 __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int token, const RowInputs& in,
-                                               const PartStats& p, int lane, bool write) {
+                                               const RowStats& p, int lane, bool write) {
   const RowScore r = row_score<FAST, ENT>(p, in.logit, a.in.c);
   const double w = in.weight, adv = in.advantage;
   const double d = static_cast<double>(in.ref_logprob) - r.logprob;
@@ -513,7 +523,9 @@ __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int
     if (a.kl != nullptr) a.kl[row] = static_cast<float>(kl);
     if (a.entropy != nullptr) a.entropy[row] = static_cast<float>(r.entropy);
   }
-  return grad_coef<FAST>(w * g, h, r.z, r.log_z, r.entropy, p.ref, a.in.c, token);
+  GradCoef k = grad_coef<FAST>(w * g, h, r.z, r.log_z, r.entropy, p.ref, a.in.c, token);
+  k.at_token = token_grad(w * g, h, r.logprob, p.rest / r.z, r.entropy, a.in.c);
+  return k;
 }
 
 // A cluster per row.  KEEP: its threads hold the row in registers between the
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
   __shared__ WarpSums warps[kWarps];
   __shared__ CarefulSums careful_warps[kWarps];
   __shared__ PartSlot slots[2][kMaxCluster];
-  __shared__ RowInputs in;  // warp 0's
+  __shared__ RowInputs in;
   __shared__ GradCoef coef;
   __shared__ int redo;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -555,7 +567,7 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     }
     GradCoef off{};
     off.token = -1;
-    if (a.grad) part_grad<T>(a.in, a.out, off, row, first, last, threadIdx.x, THREADS);
+    if (a.grad) part_grad<T, true>(a.in, a.out, off, row, first, last, threadIdx.x, THREADS);
     return;
   }
   cluster_arrive();  // this CTA runs; waited for before the first access to another's memory
@@ -565,7 +577,7 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
   float4 v[kBatch];
   int at = reader.i;
   reader.load(a.in, row, v, keep);
-  const float own_logit = swap_token(v, own, at, THREADS, -INFINITY);
+  drop_token(v, own, at, THREADS);
   if (threadIdx.x == 0) row_inputs(a, row, token, in);
   float m = -FLT_MAX;
 #pragma unroll
@@ -581,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
   while (!KEEP && reader.i < last) {
     at = reader.i;
     reader.load(a.in, row, v, keep);
-    swap_token(v, own, at, THREADS, -INFINITY);
+    drop_token(v, own, at, THREADS);
     fast_batch<ENT>(s, k, v, a.in.c.c);
   }
   fast_warp_sums<ENT>(s, k, k0, warps, warp, lane);
@@ -596,9 +608,9 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
   if (warp == 0) term = token_term(in.logit, a.in.c);  // while the sums travel
   cluster_wait();  // also: no CTA leaves while another may write to it
   if (warp == 0) {
-    PartStats p = lane_part(slots[0], lane, a.cluster);
-    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(p)) && term.holds;
-    p = add_token(merge_parts<true, kMaxCluster>(p, a.in.c), term, in.logit, a.in.c);
+    const PartStats part = lane_part(slots[0], lane, a.cluster);
+    bool ok = __all_sync(0xFFFFFFFFu, lane >= a.cluster || fast_holds(part)) && term.holds;
+    const RowStats p = add_token(merge_parts<true, kMaxCluster>(part, a.in.c), term, in.logit, a.in.c);
     ok = ok && __shfl_sync(0xFFFFFFFFu, p.z, 0) >= kFastLeast;  // the whole warp's decision
     if (ok) {
       const GradCoef g = policy_row<true, ENT>(a, row, token, in, p, lane, rank == 0);
@@ -616,7 +628,7 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     }
     cluster_sync();
     if (warp == 0) {
-      const PartStats p =
+      const RowStats p =
           add_token_careful(merge_parts<false, kMaxCluster>(lane_part(slots[1], lane, a.cluster), a.in.c), in.logit, a.in.c);
       const GradCoef g = policy_row<false, ENT>(a, row, token, in, p, lane, rank == 0);
       if (lane == 0) coef = g;
@@ -630,18 +642,17 @@ __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS
     const int i0 = first + static_cast<int>(threadIdx.x);
     SliceCursor to;
     to.start(min(i0, a.in.units - 1), a.in.per_slice);
-    swap_token(v, own, i0, THREADS, own_logit);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + u * THREADS;
       if (i < last) {
         store_unit(static_cast<T*>(a.out.grad[to.slice]) + static_cast<size_t>(row) * a.in.V_s + 4 * static_cast<size_t>(to.at),
-                   unit_grad(v[u], g, a.in.c, i), once);
+                   unit_grad<true>(v[u], g, a.in.c, i), once);
         if (i + THREADS < last) to.advance(THREADS, a.in.per_slice);
       }
     }
   } else {
-    part_grad<T>(a.in, a.out, coef, row, first, last, threadIdx.x, THREADS);
+    part_grad<T, true>(a.in, a.out, coef, row, first, last, threadIdx.x, THREADS);
   }
 }
 

@@ -300,29 +300,35 @@ __device__ __forceinline__ TokenTerm token_term(float logit, const ExpScale& c) 
   return t;
 }
 
-// A row's sums with the token's term among them; the exponentials' mean error is
-// taken out of the others'.
-__device__ __forceinline__ PartStats add_token(PartStats p, const TokenTerm& t, float logit, const ExpScale& c) {
-  const float ref = fmaxf(p.ref, t.k);
-  const double d = static_cast<double>(p.ref) - static_cast<double>(ref), f = kExpMean * exp2_int(d);
-  const double e = t.e * exp2_int(static_cast<double>(t.k) - static_cast<double>(ref));
-  p.w = (p.w + d * kLn2 * p.z) * f;
-  if (e > 0.0) p.w += e * (static_cast<double>(logit) * c.inv_t_fast - static_cast<double>(ref) * kLn2);
-  p.z = p.z * f + e;
-  p.ref = ref;
-  return p;
+// A row's sums with the token's term among them, and z without it; the
+// exponentials' mean error is taken out of the others'.
+struct RowStats {
+  double z, w, rest;
+  float ref;
+};
+__device__ __forceinline__ RowStats add_token(const PartStats& p, const TokenTerm& t, float logit, const ExpScale& c) {
+  RowStats r;
+  r.ref = fmaxf(p.ref, t.k);
+  const double d = static_cast<double>(p.ref) - static_cast<double>(r.ref), f = kExpMean * exp2_int(d);
+  const double e = t.e * exp2_int(static_cast<double>(t.k) - static_cast<double>(r.ref));
+  r.w = (p.w + d * kLn2 * p.z) * f;
+  if (e > 0.0) r.w += e * (static_cast<double>(logit) * c.inv_t_fast - static_cast<double>(r.ref) * kLn2);
+  r.rest = p.z * f;
+  r.z = r.rest + e;
+  return r;
 }
-__device__ __forceinline__ PartStats add_token_careful(PartStats p, float logit, const ExpScale& c) {
-  const float ref = fmaxf(p.ref, logit);
-  const double d = (static_cast<double>(p.ref) - static_cast<double>(ref)) * c.inv_t;
-  const double x = (static_cast<double>(logit) - static_cast<double>(ref)) * c.inv_t;
+__device__ __forceinline__ RowStats add_token_careful(const PartStats& p, float logit, const ExpScale& c) {
+  RowStats r;
+  r.ref = fmaxf(p.ref, logit);
+  const double d = (static_cast<double>(p.ref) - static_cast<double>(r.ref)) * c.inv_t;
+  const double x = (static_cast<double>(logit) - static_cast<double>(r.ref)) * c.inv_t;
   const double f = d > -1000.0 ? kExpMean * exp(d) : 0.0;
   const double e = logit < INFINITY ? (x > -1000.0 ? exp(x) : 0.0) : static_cast<double>(NAN);
-  p.w = (p.w + (d > -1000.0 ? d * p.z : 0.0)) * f;
-  if (e > 0.0) p.w += e * x;
-  p.z = p.z * f + e;
-  p.ref = ref;
-  return p;
+  r.w = (p.w + (d > -1000.0 ? d * p.z : 0.0)) * f;
+  if (e > 0.0) r.w += e * x;
+  r.rest = p.z * f;
+  r.z = r.rest + e;
+  return r;
 }
 
 // A row's results in 64 bits (a difference of two logprobs, a ratio near a
@@ -332,7 +338,7 @@ struct RowScore {
   double logprob, z, log_z, entropy;
 };
 template <bool FAST, bool ENT>
-__device__ __forceinline__ RowScore row_score(const PartStats& s, float token_logit, const ExpScale& c) {
+__device__ __forceinline__ RowScore row_score(const RowStats& s, float token_logit, const ExpScale& c) {
   RowScore r;
   r.z = s.z > 0.0 ? s.z : static_cast<double>(NAN);  // 0: every logit is -inf; NaN: a NaN or +inf logit
   r.log_z = log(r.z);
