@@ -332,7 +332,12 @@ VSL_API size_t vsl_adapters_workspace_bytes(int32_t R, int32_t n_adapters, int32
  * (bf16 inputs, fp32 sums, u carried in 24 bits).  A row whose id lies outside
  * [0, n_adapters) (-1 by convention) keeps the base logits.  A row is
  * computed from its own hidden states, its own adapter and its own logits
- * alone: infinities or NaNs of another row or adapter do not reach it.
+ * alone: infinities or NaNs of another row or adapter do not reach it, and an
+ * infinity among its own gives what the formula gives.  The rounding, and only
+ * that, depends on the batch too: R, n_adapters and the number of rows that
+ * share an adapter decide the order of the sums, so the same row in another
+ * batch may differ in its last bits (and a token drawn from it, at a near tie).
+ * The same call gives the same bits every time.
  *   logits_slices : host array of S device pointers, slice s = [R][V_s] fp32
  *                   row-major, each 16-byte aligned (vsl_logits_local's).
  *   out_slices    : the same layout; out_slices[s] may be logits_slices[s]
@@ -369,7 +374,9 @@ VSL_API vsl_status vsl_adapters_add(const float* const* logits_slices, float* co
  * convention: prompt tokens, padding, a row the sampler flagged) does not
  * count: its outputs are 0, its gradient is 0 and its logits are not read.  A
  * logit of -inf has probability 0.  A row with a NaN or +inf logit, or with
- * none above -inf, gives NaN; other rows are unaffected.
+ * none above -inf, gives NaN; other rows are unaffected.  R and S * V_s decide
+ * the order of a row's sums: the same row in a batch of another size may differ
+ * in its last bits; the same call gives the same bits every time.
  * The temperature T is one number per call, 1e-6 <= T <= 1e6. */
 
 /* vsl_token_logprobs - the logprob (and entropy) of one given token per row.

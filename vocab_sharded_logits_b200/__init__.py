@@ -430,7 +430,8 @@ def adapters_add(logits_slices, hidden, a, b_slices, adapter_ids, scale=None, ou
     With ``tile_stats`` (True, or a tensor to fill) the tile statistics of the result are written
     too, and the call returns ``(slices, stats)``.  workspace: a uint8 tensor of
     ``adapters_workspace_bytes(R, n, rank)`` bytes (None: allocated for the call); calls that may run
-    at the same time need one each.
+    at the same time need one each.  The batch a row is in (its size, the rows that share its adapter)
+    decides the order of its sums and so its last bits, nothing else of it.
     """
     stats = None
     if tile_stats is not None and tile_stats is not False:
@@ -457,7 +458,8 @@ def token_logprobs(logits_slices, token_ids, temperature=1.0, entropy=False, out
     the row's entropy.
 
     logits_slices: list of fp32 [R, V_s] CUDA tensors; token_ids: int32 [R] (outside the vocabulary,
-    -1 by convention: the row does not count, its outputs are 0).  out: a ``TokenLogprobs`` to fill
+    -1 by convention: the row does not count, its outputs are 0).  The number of rows decides the order
+    of a row's sums and so its last bits.  out: a ``TokenLogprobs`` to fill
     again (its entropy too, where it holds one; a logprob or row_stats that is None is made).
     """
     if out is None:

@@ -19,10 +19,16 @@
 // What it cannot do without: one read and one write of the logits and one read
 // of each used adapter's A and B.  Measured (H = 4,096 but where stated, of the
 // time those bytes take at the 6.56 TB/s of a copy): one row of rank 16 over
-// 151,936 ids 8.3 us (two launches, one of which waits for the other's end); 64
-// rows of as many adapters of rank 16 76 us, 80 %; 512 rows over 24 adapters of
-// rank 32 167 us, 189 with tile statistics, 67 %; 2,048 rows over 8 adapters of
-// rank 64 (H = 5,120) 675 us, 60 %.
+// 151,936 ids 7.5 us (two launches, one of which waits for the other's end); 64
+// rows of as many adapters of rank 16 73 us, 83 %; 512 rows over 18 adapters of
+// rank 32 159 us, 78 %, 184 with tile statistics, 68 %; 2,048 rows over 8
+// adapters of rank 64 (H = 5,120) 631 us, 65 %.
+//
+// Times here and below, but where another is named: calls with given outputs,
+// replayed back to back from a graph over the same tensors, the median of five
+// allocations.  One allocation differs from another by up to 5 % above 100 us.  A
+// program that calls from Python over changing inputs sees 10 us for the one row
+// and 672 for the 2,048.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -53,9 +59,9 @@ constexpr int kFewRows = 2;       // see few_rows_of
 __host__ __device__ constexpr int rank_steps(int rank) { return rank <= 16 ? 1 : (rank + 31) / 32 * 2; }
 // Units of at most so many rows are done with float32 multiply-adds: of 16 rows
 // of a product 14 or more would be empty, and u is as long as a lane's own share
-// of it.  64 rows of as many adapters of rank 16: 78 us, 111 by products; 32
-// adapters of two rows 54, 68; at rank 32 127 and 138, 80 and 82; at rank 64
-// it is the products that are faster, 234 us (284) and 130 (168).
+// of it.  64 rows of as many adapters of rank 16: 73 us, 102 by products; 32
+// adapters of two rows 52, 65; at rank 32 126 and 139, but 79 and 77; at rank 64
+// the products are as fast, 245 us (245), or faster, 135 (151).
 __host__ __device__ constexpr int few_rows_of(int rank) { return rank <= 32 ? kFewRows : 0; }
 // Units a tile of `rows` rows over n adapters can have: full ones, a ragged one
 // per adapter and one of rows without an adapter.
@@ -106,9 +112,9 @@ struct ShrinkArgs {
 // part, the CTAs of a cluster share H.  Every CTA sorts the tile itself, by
 // counting, which costs less than a launch that does it once.  Bound by the
 // latency of its chain (ids, sort, one run over H, the warps' sums, the
-// cluster's): 21 us for 512 rows over 24 adapters of rank 32, 42 us for 2,048
-// over 8 of rank 64 (H = 5,120); the second kernel's CTAs are already there when
-// it ends.
+// cluster's): 21 us for 512 rows over 18 adapters of rank 32, 45 us for 2,048
+// over 8 of rank 64 (H = 5,120), each alone under the profiler; the second
+// kernel's CTAs are already there when it ends.
 __global__ void __launch_bounds__(kShrinkWarps * 32) adapters_shrink_kernel(const __grid_constant__ ShrinkArgs p) {
   __shared__ int key[kTile];
   __shared__ int order[kTile];        // sorted position -> row of the tile
@@ -543,7 +549,7 @@ constexpr size_t expand_smem() {
   return kStages * sizeof(ExpandStage<STEPS>);
 }
 // CTAs that the registers let stand on an SM (512 rows of rank 32 with statistics:
-// 189 us with 13, 204 with 16, 225 with 12, rank 64 no different with fewer).
+// 184 us with 13, 195 with 16, 198 with 12, rank 64 no different with fewer).
 constexpr int expand_ctas(int steps) { return steps == 4 ? 12 : steps == 2 ? 13 : 16; }
 
 // A warp's unit: its plan entry, and where its u is.
@@ -633,8 +639,8 @@ __device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)
 }
 
 // A CTA is one warp: a unit whose rows are few, or a slot that is empty, holds no
-// other warp's place (one row of rank 16: 8.3 us, 10.4 with four warps a CTA; 64
-// requests 76 us, 78).
+// other warp's place (when it was chosen, of this kernel's form then: one row of
+// rank 16 8.3 us, 10.4 with four warps a CTA; 64 requests 76 us, 78).
 //
 // The warp takes a unit's 16 rows and runs over blocks of 128 ids (of a slice), a
 // quarter at a time, the next quarters' logits and B on their way meanwhile.
@@ -642,14 +648,15 @@ __device__ __forceinline__ void store_quarter(float* dst, const size_t (&row_at)
 // consecutive ids of a row: column n of the i-th product of 4 is id
 // 16 (i / 2) + 4 (n / 2) + 2 (i mod 2) + n mod 2.
 //
-// 512 rows over 24 adapters of rank 32 with statistics: 171 us, 0.78 GB of DRAM
-// traffic (4.6 TB/s), the issue slots 56 % used.  2,048 rows over 8 adapters of
-// rank 64: 559 us, 2.64 GB (4.7 TB/s), the tensor pipe 45 % active, 7.5 GB
-// through the L2 cache, where the B's of 155 MB are read once for each unit of
-// 16 rows.  No unit is full; what is left is their overlap within a warp, which
-// waits for copies, products and sums in turn.  Units of 32 rows, which read B
-// half as often, need twice the registers: 612 us where this takes 591; more
-// warps, more stages or B through L1 left the time as it was or cost up to 10 %.
+// Under the profiler, alone: 512 rows over 18 adapters of rank 32 with statistics
+// 172 us, 0.78 GB of DRAM traffic (4.5 TB/s), the issue slots 57 % used; 2,048
+// rows over 8 adapters of rank 64 565 us, 2.64 GB (4.7 TB/s), the tensor pipe 45 %
+// active, 5.6 GB read out of the L2 cache (176 M sectors), where the B's of 155 MB
+// are read once for each unit of 16 rows.  What is left is the overlap within a
+// warp, which waits for copies, products and sums in turn, and that reading of B.
+// Units of 32 rows, which read B half as often, need twice the registers: when
+// they were tried 612 us where this took 591; more warps, more stages or B
+// through L1 left the time as it was or cost up to 10 %.
 template <int STEPS, int LANES>  // rank_steps, lanes of 8 ranks in few_rows (0: no unit comes there)
 __global__ void __launch_bounds__(32, expand_ctas(STEPS))
     adapters_expand_kernel(const __grid_constant__ ExpandArgs p) {
@@ -830,9 +837,10 @@ __global__ void __launch_bounds__(32, expand_ctas(STEPS))
 
 // The same for ranks above 64: B and u are loaded as they are used, so that the
 // time is the loads' latency over the warps that stand on an SM (512 rows over 8
-// adapters: 354 us at rank 128, 590 at rank 256; 2.6 and 2.1 TB/s).  The small
-// terms' sums stay apart here too; their 16 registers cost a tenth (324 and 525
-// us in one sum, which loses them where the large terms cancel the logit).
+// adapters: 356 us at rank 128, 599 at rank 256; 2.6 and 2.1 TB/s).  The small
+// terms' sums stay apart here too; their 16 registers cost a tenth (called from
+// Python 324 us became 354, 525 590), but one sum loses them where the large terms
+// cancel the logit.
 __global__ void __launch_bounds__(kWideWarps * 32, 16 / kWideWarps) adapters_expand_wide_kernel(const __grid_constant__ ExpandArgs p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -948,8 +956,8 @@ cudaError_t prepare_expand() {
       if (status[dev] == cudaSuccess)
         status[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       // The rest is L1, which the multiply-adds' loads need (64 requests of rank
-      // 32: 129 us, 148 with 196 KB; of rank 16 76 us, 90), and no case wants
-      // more warps than fit (2,048 rows of rank 64: 591 us, 595 with 228 KB).
+      // 32: 126 us, 144 with 196 KB; of rank 16 73 us, 87), and no case wants
+      // more warps than fit (2,048 rows of rank 64: 631 us, 638 with 228 KB).
       if (status[dev] == cudaSuccess)
         status[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
     };
@@ -986,8 +994,8 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   sa.rank = rank;
   sa.slots = z.slots;
   // the CTAs of a cluster share longer rows of H while the units are few (one row
-  // of rank 16 over H = 4,096: 10.4 us, 14.5 by one CTA; 512 rows over 24 adapters
-  // of rank 32: 172 us, 194)
+  // of rank 16 over H = 4,096: 7.5 us, 12.4 by one CTA; 512 rows over 18 adapters
+  // of rank 32 with statistics: 184 us, 191)
   const int steps = rank_steps(rank);
   const long long ctas = static_cast<long long>(z.tiles) * z.slots * steps;
   sa.split = H < 4 * 256 || ctas > 296 ? 1 : ctas > 148 ? 2 : kMaxSplit;
@@ -1025,14 +1033,14 @@ cudaError_t launch_adapters_add(const float* const* logits, float* const* out, c
   ea.slots = z.slots;
   ea.tiles = z.tiles;
   // Above rank 64 the warps of a CTA, next units, read the same B out of L1 where
-  // adapters have units enough (512 rows over 8 adapters of rank 128: 325 us, 338
-  // by single warps; 16 over 16: 146, 142; one row of rank 256: 43, 29).
+  // adapters have units enough (512 rows over 8 adapters of rank 128: 356 us, 375
+  // by single warps; 16 over 16: 160, 164; one row of rank 256: 46, 32).
   const int warps = rank > 64 && R > kUnitRows * static_cast<long long>(n) ? kWideWarps : 1;
   ea.slot_ctas = static_cast<int>((static_cast<long long>(z.tiles) * z.slots + warps - 1) / warps);
   // A warp keeps its unit's u over several blocks, while there are warps enough
-  // to fill the SMs some times over (64 requests of rank 16: 78 us, 94 with a
-  // block a warp; 2,048 rows over 8 adapters of rank 64: 620 us, 712).  Above
-  // rank 64 it keeps no u (512 rows of rank 256: 545 us, 577 with several blocks).
+  // to fill the SMs some times over (64 requests of rank 16: 73 us, 87 with a
+  // block a warp; 2,048 rows over 8 adapters of rank 64: 631 us, 719).  Above
+  // rank 64 it keeps no u (512 rows of rank 256: 599 us, 626 with four blocks).
   ea.warp_blocks = 1;
   while (rank <= 64 && ea.warp_blocks < 8 && static_cast<long long>(ea.slot_ctas) * S * ea.B / ea.warp_blocks > 8 * 148 * 16)
     ea.warp_blocks *= 2;

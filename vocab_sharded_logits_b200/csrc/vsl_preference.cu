@@ -11,7 +11,8 @@
 // cancels.
 //
 // One CTA per pair: 8 bytes read and 4 written per row, bound by launch latency
-// and the chain of offsets, sums and loss (a pair of 256 rows each: 8 us).
+// and the chain of offsets, sums and loss (a pair of 256 rows each: 3.4 us in a
+// graph's replay, 6.5 alone and cold).
 #include <cuda_runtime.h>
 
 #include <cmath>

@@ -13,6 +13,10 @@
 //   G_j = e_j (alpha + gamma log e_j) + (g / T) 1[j = t].
 // Clipped policy loss of a row with ratio r = exp(logp - old):
 //   w [ -min(r A, clip(r, 1 - lo, 1 + hi) A) + beta (exp(d) - d - 1) - c H ],  d = ref - logp.
+//
+// Times below, but where another is named: calls replayed back to back from a
+// graph over the same tensors, the median of five allocations.  One allocation
+// differs from another by up to 5 % above 100 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -327,9 +331,9 @@ struct LogprobArgs {
 
 // A cluster per row: each CTA streams a part of the row once; the CTAs exchange
 // their sums over distributed shared memory.  Bound by DRAM where there are rows
-// enough (2,048 of 151,936: 187 us, 6.6 TB/s; 512: 53 us, 5.9 TB/s, the last,
+// enough (2,048 of 151,936: 194 us, 6.4 TB/s; 512: 51 us, 6.1 TB/s, the last,
 // partial set of CTAs in it), by the chain of load, sums, exchange and the row's
-// arithmetic where there are few (64 rows of 248,320: 15 us; 4 of 1,024: 4.3 us).
+// arithmetic where there are few (64 rows of 248,320: 12.7 us; 4 of 1,024: 4.5 us).
 template <bool ENT, int THREADS>
 __global__ void __launch_bounds__(THREADS, kLogprobThreads / THREADS)
     token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
@@ -439,7 +443,8 @@ struct LogprobGradArgs {
 
 // Four CTAs of 512 threads an SM, each 8 units of a row a thread, two loads in
 // flight: no sum is shared, so the work is cut finely.  Bound by DRAM: 512 rows of
-// 151,936 96 us to float32 (6.5 TB/s of one read and one write), 81 us to bf16 (5.7).
+// 151,936 100 us to float32 (6.2 TB/s of one read and one write), 85 us to bf16
+// (5.5); with the entropy's derivative 103 and 89.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) token_logprobs_grad_kernel(const __grid_constant__ LogprobGradArgs a) {
   const int row = static_cast<int>(blockIdx.x) / a.parts;
@@ -532,16 +537,16 @@ __device__ __forceinline__ GradCoef policy_row(const PolicyArgs& a, int row, int
 // two passes.  Else its CTAs stream the row once for the sums, exchange them
 // over distributed shared memory, and read their parts again for the gradient,
 // out of the L2 cache: the first reading asks it to keep the lines, the second
-// and the gradient's stores to let theirs go first (2,048 rows of 151,936: 486 us,
-// 563 if the first asks nothing).
+// and the gradient's stores to let theirs go first (2,048 rows of 151,936: 517 us,
+// 519 if the first asks nothing).
 //
-// DRAM sees the row once (512 rows of 151,936: 350 MB read of 311 without the
-// second reading, 279 MB written): 132 us to float32, 107 to bf16; 2,048 rows
-// 486 and 385 us, 5.1 and 4.9 TB/s.  What bounds it is that a row's phases wait
+// DRAM sees the row once (512 rows of 151,936: 347 MB read of 311 without the
+// second reading, 259 MB written): 135 us to float32, 115 to bf16; 2,048 rows
+// 517 and 432 us, 4.8 and 4.3 TB/s.  What bounds it is that a row's phases wait
 // on one another (read, exchange, the row's arithmetic in 64 bits, read and
 // write): the rows beside it on the SM fill the gaps only in part.  A form that
 // kept the row in a cluster's shared memory, fed by TMA through a ring, took 588
-// us for the 2,048 rows: fewer rows at a time, longer gaps.
+// us for the 2,048 rows where this took 495 then: fewer rows at a time, longer gaps.
 template <typename T, bool ENT, bool KEEP, int THREADS>
 __global__ void __launch_bounds__(THREADS, (KEEP ? 1024 : kRowThreads) / THREADS)
     policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
@@ -683,14 +688,15 @@ cudaError_t device_sms(int* sms) {
 }
 
 // Threads of a CTA of the row kernels.  CTAs of 256 finish and make room in
-// smaller steps than of 512 (logprobs of 512 rows of 151,936: 53 us, 64 with
-// 512; of 2,048: 184 us, 201; policy loss of 300 rows of 51,012: 32 us, 35), of
-// 128 only pay on short rows (512 rows of 8,000: 8 us with 128, 10 with 512;
-// 512 rows of 151,936: policy loss 148 us with 128, 133 with 256).  512 where
-// the rows are so few that a CTA each SM's worth would not fill them (policy
-// loss of 16 rows of 262,144: 16.5 us, 18.5 with 256), and in the policy loss
-// where 256 would leave more rows in flight than the L2 cache holds (1,024 rows
-// of 262,144: 424 us, 438).
+// smaller steps than of 512 (logprobs of 512 rows of 151,936: 51 us, 64 with
+// 512; of 2,048: 194 us, 207; policy loss of 300 rows of 51,012: 30 us, 32), of
+// 128 only pay on short rows where there are many (logprobs of 4,000 rows of
+// 2,000: 11 us with 128, 19 with 256; of 8,000 25, 30; but of 512 rows 5.1 and
+// 6.1 with 128, 4.3 and 5.6 with 256; policy loss of 512 rows of 151,936: 149 us
+// with 128, 135 with 256).  512 where the rows are so few that a CTA each SM's
+// worth would not fill them (policy loss of 16 rows of 262,144: 15.6 us, 16.8
+// with 256), and in the policy loss where 256 would leave more rows in flight
+// than the L2 cache holds (1,024 rows of 262,144: 450 us, 465).
 constexpr float kL2Room = 96.0f * 1048576.0f;  // of 126 MB
 int row_threads(int R, int units, bool cached, int sms) {
   if (units <= 2048) return 128;
@@ -707,9 +713,9 @@ int row_threads(int R, int units, bool cached, int sms) {
 // share, but not faster than a third.  Both constants are fits to measured
 // times, and only their ratio matters: it keeps, say, 148 rows from taking 4
 // CTAs each, a third more than there are places (policy loss of 148 rows of
-// 151,936, CTAs of 512: 51 us with 4, 45 with 2).  `cached`: the rows being worked on at a
+// 151,936, CTAs of 512: 50 us with 4, 44 with 2).  `cached`: the rows being worked on at a
 // time must leave the L2 cache room, at most 96 MB of its 126 (2,048 rows of
-// 151,936: 486 us; 544 with room for 140 MB, 584 with 64).
+// 151,936: 517 us; 550 with room for 140 MB, 610 with 64).
 cudaError_t choose_cluster(int R, int units, float per_unit, float fixed, bool cached, int* cluster, int* threads_out) {
   int sms = 0;
   const cudaError_t e = device_sms(&sms);
@@ -739,8 +745,8 @@ cudaError_t row_cluster(int R, int units, int* cluster, int* threads) {
 
 // keep: the threads hold their parts in registers between the two passes,
 // which pays where all CTAs run at once and time is latency (4 rows of 1,024:
-// 6.3 us, 8.4 without), not where it halves how many do (300 rows of 51,012, CTAs
-// of 512: 73 us, 35 without).
+// 5.2 us, 5.6 without; 64 rows 5.4, 5.9), not where it halves how many do (300
+// rows of 51,012, eight CTAs of 512: 66 us, 55 without).
 cudaError_t policy_cluster(int R, int units, int* cluster, int* threads, bool* keep) {
   const cudaError_t e = choose_cluster(R, units, 1.1f, 6.0f, true, cluster, threads);
   if (e != cudaSuccess) return e;
