@@ -166,3 +166,32 @@ def test_the_gradient_at_a_token_on_top(cuda_device, V, S, ent_coef, height):
     off = np.abs(np.concatenate([_np(x) for x in grad], 1)[rows, top] - exact)
     bound = (1 + 2 * ent_coef) * (2.0 ** -22 + 6 * STEP) + rest * eps + ent_coef * ((rest + size) * eps + STEP * ent)
     assert (off <= bound).all(), (off / bound).max()
+
+
+@pytest.mark.parametrize("low", [-23.0, -25.0, -27.0, -100.0, -600.0, -2000.0])
+@pytest.mark.parametrize("V,S", SIZES)
+def test_rows_far_below_zero(cuda_device, V, S, low):
+    """The top one at `low`, the row's token 1 below it, the others far down: as near 0 as far from it, the top one's
+    exponential is what the logprob rests on."""
+    rng = np.random.default_rng([V, int(-low)])
+    l = (rng.normal(size=(16, V)) * 2 + low - 30).astype(np.float32)
+    rows, top = np.arange(16), np.arange(16) * (V // 16) + 5
+    tok = ((top + V // 2 + 3) % V).astype(np.int32)
+    l[rows, top] = (low + np.arange(16) / 37.0).astype(np.float32)
+    l[rows, tok] = l[rows, top] - np.float32(1.0)
+    logp = O.log_softmax(l)
+    lp, ent = O.token_logprobs(l, tok)
+    p = np.exp(logp)
+    p[rows, tok] = p[rows, top] = 0.0
+    rest = p.sum(1)
+    of_top = 2.0 ** -22 + 2 * STEP + 2.0 ** -22 * np.log(2) + 2 * STEP
+    bound = of_top + 2 * rest + STEP * np.abs(lp)
+    slices, t = _slices(l, S, cuda_device), torch.from_numpy(tok).to(cuda_device)
+    one = torch.ones(16, device=cuda_device)
+    fwd = vsl.token_logprobs(slices, t, entropy=True)
+    pol = vsl.policy_loss(slices, t, _dev(lp, cuda_device), one, entropy_coef=0.01)
+    for got in (fwd, pol):
+        off = np.abs(_np(got.logprob) - lp)
+        assert (off <= bound).all(), (off / bound).max()
+        off = np.abs(_np(got.entropy) - ent)
+        assert (off <= 3 * of_top + 8 * STEP + 80 * rest + STEP * ent).all(), off.max()

@@ -21,8 +21,7 @@
 // in its exponential, one below 5 has 2^-22 at most.  Different k are powers of
 // two apart, so bringing sums together costs no rounding.  What it rests on is
 // checked afterwards: a row whose sums left [2^-40, 2^60] (a NaN or +inf logit;
-// none above -inf; all of them some 28 T below 0) or whose k exceeds 2^20 is
-// done again in the careful form.  c's rounding is a temperature off by at
+// none above -inf) or whose k exceeds 2^20 is done again in the careful form.  c's rounding is a temperature off by at
 // most 2^-24, used consistently: log p_t moves by at most 2^-24 of its distance
 // from the mean of x.
 //
@@ -125,13 +124,13 @@ struct FastSums {
   float2 z, w;
 };
 
-// The CTA's k from the largest of the logits its threads read first.  Far
-// below 0 these are masked ones, as a rule: what follows is likely near 0.
+// The CTA's k from the largest of the logits its threads read first (0 where
+// that is lower than k may be, as masked ones are).
+constexpr float kFastMaxK = 1048576.0f;
 __device__ __forceinline__ float fast_reference(float top, float c) {
   const float k = rintf(top * c);
-  return k < -30.0f ? 0.0f : k;
+  return k < -kFastMaxK ? 0.0f : k;
 }
-constexpr float kFastMaxK = 1048576.0f;
 
 // Four logits.
 template <bool ENT>
